@@ -62,7 +62,8 @@ typedef enum lsa_status {
 
 typedef enum lsa_dtype {
   LSA_BF16 = 0,
-  LSA_E4M3 = 1
+  LSA_E4M3 = 1,
+  LSA_FP32 = 2 /* lsa_rope only */
 } lsa_dtype_t;
 
 /* Streaming-aware budget [LSA abstract (1); LSA limitations; CARD "SI"]:
@@ -140,8 +141,113 @@ typedef enum lsa_op {
   LSA_OP_SELECT = 2,
   LSA_OP_SPARSE_ATTN = 3,
   LSA_OP_LAYER_GROUP = 4,
-  LSA_OP_INDEX_COMPRESSED = 5
+  LSA_OP_INDEX_COMPRESSED = 5,
+  LSA_OP_PAGED_ATTN = 6,
+  LSA_OP_PAGES_FORK = 7,
+  LSA_OP_PAGES_COPY = 8,
+  LSA_OP_PAGES_COMPACT = 9
 } lsa_op_t;
+
+/* ------------------------------------------------------- the paged cache --
+ * A cache whose rows live in pages of P tokens. A pool holds n_pages pages; the
+ * block table [S, max_pages] int32 gives the physical page of each logical page
+ * of a sequence (token s lies in logical page s / P, slot s % P), -1 where none
+ * is mapped. The mapped entries of a row form a prefix. ref [n_pages] int32
+ * counts the sequences that hold a page; a page with ref 0 is free. One table
+ * serves any number of pools (keys, values, scales, every layer).
+ * Calls with T new tokens per sequence take q_len [B] (device int32, or NULL
+ * for T each): token t < q_len[b] of sequence b sits at position
+ *   pos(b, t) = seq_len[b] - q_len[b] + t,
+ * seq_len counting the new tokens too; tokens with t >= q_len[b] or pos < 0
+ * are padding. q_len is clamped to [0, T].
+ * Page ids, sequence ids and table entries outside their range are skipped and
+ * make the next lsa_device_status() return LSA_ERR_INVALID_ARG.
+ * Page sizes P: 16, 32, 64, 128. n_pages <= LSA_MAX_PAGES; S <= LSA_MAX_SEQS. */
+#define LSA_MAX_PAGES (1 << 19)
+#define LSA_MAX_SEQS 8192
+#define LSA_ROPE_MAX_PAIRS 128
+
+typedef enum lsa_rope_scaling {
+  LSA_ROPE_PLAIN = 0,  /* f_i = theta^(-2i / rot) */
+  LSA_ROPE_LINEAR = 1, /* f_i / factor (positions interpolated) */
+  LSA_ROPE_YARN = 2    /* by frequency (YaRN, arXiv 2309.00071, section 3) */
+} lsa_rope_scaling_t;
+
+/* Rotary frequencies, filled by lsa_rope_plan; host memory, passed by pointer
+ * and copied into each launch. */
+typedef struct lsa_rope_plan {
+  int32_t rot_dim, interleaved;
+  double amplitude;
+  double freq[LSA_ROPE_MAX_PAIRS]; /* radians per position of pair i */
+} lsa_rope_plan_t;
+
+/* Rows to rotate: x [B,T,H,d] and out alike, bf16 or fp32. Strides in elements
+ * (the last dimension is dense); out may be x with x's strides. Columns
+ * [offset, offset + rot_dim) are rotated; the others are copied. */
+typedef struct lsa_rope_in {
+  int32_t B, T, H, d;
+  int32_t dtype;   /* LSA_BF16 or LSA_FP32 */
+  int32_t offset;
+  int32_t inverse; /* 1: the transposed rotation (the gradient of x from that of out) */
+  const int32_t* seq_len;
+  const int32_t* q_len;
+  const void* x;
+  int64_t x_stride_b, x_stride_t, x_stride_h;
+  int64_t out_stride_b, out_stride_t, out_stride_h;
+} lsa_rope_in_t;
+
+/* New rows for a paged cache: x [B,T,H,d] bf16, dense. The pool's row of a
+ * token is H*d elements, rows row_stride and pages page_stride elements apart
+ * (multiples of 16 bytes). dtype LSA_BF16, or LSA_E4M3 with scales
+ * [n_pages, P] fp32: scale = amax / 448 over the (rotated) row, or 1 for a row
+ * of zeros; code = e4m3(x / scale), RNE, saturating. d and offset are multiples
+ * of 8, rot_dim of 16; e4m3 rows: H * d <= 1024 and a multiple of 16. */
+typedef struct lsa_append_in {
+  int32_t B, T, H, d;
+  int32_t n_pages, page_size, max_pages;
+  int32_t dtype;
+  int32_t offset; /* first rotated column (plan given) */
+  const int32_t* seq_len;
+  const int32_t* q_len;
+  const int32_t* table; /* [B, max_pages] */
+  const void* x;
+  void* pool;
+  int64_t page_stride, row_stride;
+  float* scales; /* LSA_E4M3: [n_pages, page_size]; else NULL */
+} lsa_append_in_t;
+
+/* Attention of the new tokens over every cached token they see:
+ *   o[b,t,h] = sum_{s <= pos(b,t)} softmax_s(scale * q[b,t,h] . K[b,s,g]) V[b,s,g],
+ *   g = h / (Hq / Hkv),
+ * K row of token s: k + table[b, s / P] * k_page_stride + (s % P) * k_row_stride
+ * + g * d_qk (elements), V alike. Supported: (d_qk, d_v) = (64, 64) and
+ * (128, 128), bf16, Hq a multiple of Hkv; and latent rows (576, 512) with v = k, Hkv = 1,
+ * Hq <= 128, bf16 or LSA_E4M3 (K = V = code * k_scale[page, slot], fp32).
+ * q [B,T,Hq,d_qk] bf16, dense. Tokens of unmapped pages are left out. What a
+ * page holds at and past seq_len is never used, whatever its bits; the rows of
+ * cached tokens must be finite. A seq_len past the table's max_pages * P tokens
+ * is clamped and reported. */
+typedef struct lsa_paged_attn_in {
+  int32_t B, T, Hq, Hkv, d_qk, d_v;
+  int32_t n_pages, page_size, max_pages;
+  float scale;
+  int32_t kv_dtype;
+  const int32_t* seq_len;
+  const int32_t* q_len;
+  const int32_t* table; /* [B, max_pages] */
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t k_page_stride, k_row_stride, v_page_stride, v_row_stride;
+  const float* k_scale;
+} lsa_paged_attn_in_t;
+
+/* One pool: page p is the page_bytes bytes at base + p * page_stride (bytes,
+ * both multiples of 16). */
+typedef struct lsa_pool {
+  void* base;
+  int64_t page_bytes, page_stride;
+} lsa_pool_t;
 
 /* Arguments of lsa_workspace_size; fill the members the op uses. */
 typedef struct lsa_op_args {
@@ -153,6 +259,9 @@ typedef struct lsa_op_args {
   int32_t B, T, L_max;             /* SELECT */
   int32_t scores_external;         /* INDEX_FLAT, INDEX_COMPRESSED: 1 if the caller passes scores_out */
   int32_t m;                       /* INDEX_COMPRESSED: tokens per entry */
+  const lsa_paged_attn_in_t* paged; /* PAGED_ATTN */
+  int32_t n;                       /* PAGES_FORK, PAGES_COPY: pairs */
+  int32_t n_pages;                 /* PAGES_COMPACT */
 } lsa_op_args_t;
 
 /* One-line description of a status code (static storage). */
@@ -310,10 +419,84 @@ lsa_status_t lsa_layer_group(const lsa_indexer_in_t* in, const void* page_keys, 
                              float* const* lse_outs, int32_t* idx, void* workspace,
                              size_t workspace_bytes, lsa_stream_t stream);
 
+/* Frequencies of a rotary embedding of rot_dim columns (even, <= 256) as pairs
+ * (2i, 2i+1) (interleaved) or (i, i + rot_dim/2). LSA_ROPE_YARN blends f_i and
+ * f_i / factor by a ramp over i between the pairs that turn beta_fast and
+ * beta_slow times in orig_len positions. amplitude multiplies the rotated
+ * columns; 0 = the default (0.1 ln factor + 1 for YaRN with factor > 1, else 1).
+ * Host arithmetic in 64 bits. */
+lsa_status_t lsa_rope_plan(int32_t rot_dim, int32_t interleaved, double theta, lsa_rope_scaling_t scaling,
+                           double factor, int32_t orig_len, double beta_fast, double beta_slow,
+                           double amplitude, lsa_rope_plan_t* plan);
+
+/* Rotary positions: for pair i of a row at position pos, a = pos * f_i,
+ *   y0 = m (x0 cos a - x1 sin a),  y1 = m (x1 cos a + x0 sin a)
+ * (inverse: -a). The angle is reduced in 64 bits, the product taken in fp32 and
+ * rounded once. Rows of padding tokens of out are left as they were. */
+lsa_status_t lsa_rope(const lsa_rope_in_t* in, const lsa_rope_plan_t* plan, void* out, lsa_stream_t stream);
+
+/* Writes the new rows into their pages, rotated first if plan is not NULL
+ * (every head's columns [offset, offset + rot_dim)). Padding tokens and tokens
+ * of unmapped pages write nothing (the latter are reported). A page must not be
+ * shared where it is written (lsa_pages_fork copies the partly filled page). */
+lsa_status_t lsa_pages_append(const lsa_append_in_t* in, const lsa_rope_plan_t* plan, lsa_stream_t stream);
+
+/* Attention over the paged cache (lsa_paged_attn_in_t). out [B,T,Hq,d_v] bf16;
+ * lse [B,T,Hq] fp32 optional. A query that sees no token (pos < 0, or only
+ * unmapped pages) gets out = 0, lse = -inf; rows t >= q_len[b] are left as they
+ * were. */
+lsa_status_t lsa_paged_attn(const lsa_paged_attn_in_t* in, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, lsa_stream_t stream);
+
+/* Maps pages until each sequence's row holds len[s] tokens: the lowest free
+ * pages, in (sequence, logical page) order, with ref = 1. When free pages run
+ * out, what is left stays unmapped and lsa_device_status() returns
+ * LSA_ERR_WORKSPACE. A len beyond max_pages * P is clamped and reported. */
+lsa_status_t lsa_pages_reserve(int32_t* table, int32_t* ref, const int32_t* len, int32_t S, int32_t max_pages,
+                               int32_t n_pages, int32_t page_size, lsa_stream_t stream);
+
+/* Forks sequences: child[i] becomes a copy of parent[i] (n pairs, device
+ * int32). Full pages are shared (ref + 1); a partly filled last page is copied,
+ * in every pool, into the lowest free page (in pair order). The child's table
+ * row is overwritten, so its pages have to be free before; pages reserved past
+ * seq_len[parent] are not handed on. A parent may repeat. A pair is skipped and
+ * reported if an id is out of range, an earlier pair has the same child, or the
+ * parent is itself a child of this call. Without a free page left the child
+ * keeps the full pages only, with seq_len cut to them (reported as by
+ * lsa_pages_reserve). */
+lsa_status_t lsa_pages_fork(int32_t* table, int32_t* ref, int32_t* seq_len, int32_t S, int32_t max_pages,
+                            int32_t n_pages, int32_t page_size, const int32_t* parent, const int32_t* child,
+                            int32_t n, const lsa_pool_t* pools, int32_t n_pools, void* workspace,
+                            size_t workspace_bytes, lsa_stream_t stream);
+
+/* Frees sequences (n ids, device int32): every mapped page's ref - 1, the row
+ * unmapped, seq_len 0. An id that repeats is freed once. */
+lsa_status_t lsa_pages_free(int32_t* table, int32_t* ref, int32_t* seq_len, int32_t S, int32_t max_pages,
+                            int32_t n_pages, const int32_t* seqs, int32_t n, lsa_stream_t stream);
+
+/* Copies page src[i] to page dst[i] in every pool (n pairs, device int32). All
+ * pairs act at once: a pair is skipped and reported if an id is out of range,
+ * its dst occurs more than once, or its dst is some pair's src. */
+lsa_status_t lsa_pages_copy(const lsa_pool_t* pools, int32_t n_pools, int32_t n_pages, const int32_t* src,
+                            const int32_t* dst, int32_t n, void* workspace, size_t workspace_bytes,
+                            lsa_stream_t stream);
+
+/* Packs the live pages (ref > 0) into the first n_live: the k-th live page at
+ * or above n_live moves to the k-th hole below it, in every pool, and table
+ * entries and counts follow. table_out [S, max_pages] and ref_out [n_pages] may
+ * be table and ref themselves; n_live (device int32) is optional. The pages
+ * left behind keep their old contents. */
+lsa_status_t lsa_pages_compact(const int32_t* table, const int32_t* ref, int32_t S, int32_t max_pages,
+                               int32_t n_pages, const lsa_pool_t* pools, int32_t n_pools, int32_t* table_out,
+                               int32_t* ref_out, int32_t* n_live, void* workspace, size_t workspace_bytes,
+                               lsa_stream_t stream);
+
 /* Synchronises `stream`, then returns and clears the device status word of the
  * current device, for everything since the last call: LSA_OK; LSA_ERR_TIMEOUT
  * if a kernel gave up waiting; LSA_ERR_INVALID_ARG if an attention index row
- * held an entry >= L_max; LSA_ERR_CUDA if an internal bound did not hold. */
+ * held an entry >= L_max, or a page, sequence or table entry was out of range;
+ * LSA_ERR_WORKSPACE if a paged cache ran out of free pages; LSA_ERR_CUDA if an
+ * internal bound did not hold. */
 lsa_status_t lsa_device_status(lsa_stream_t stream);
 
 #ifdef __cplusplus

@@ -10,4 +10,6 @@ from .lsa import (  # noqa: F401
     lsa_index_flat, lsa_select_streaming, lsa_pool_pages, lsa_index_hier,
     lsa_sparse_attn, lsa_layer_group, lsa_device_status, lsa_pool_pages_e4m3, lsa_index_hier_e4m3,
     lsa_select_streaming_noalloc, lsa_index_compressed,
+    lsa_rope_plan, lsa_rope, lsa_pages_append, paged_attn_in, lsa_paged_attn, lsa_pages_reserve, lsa_pages_fork,
+    lsa_pages_free, lsa_pages_copy, lsa_pages_compact,
 )

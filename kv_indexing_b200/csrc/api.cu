@@ -692,6 +692,12 @@ lsa_status_t lsa_workspace_size(lsa_op_t op, const lsa_op_args_t* args, size_t* 
       *bytes = idx_bytes + ix + at;
       return LSA_OK;
     }
+    case LSA_OP_PAGED_ATTN:
+      return paged_attn_workspace(args->paged, bytes);
+    case LSA_OP_PAGES_FORK:
+    case LSA_OP_PAGES_COPY:
+    case LSA_OP_PAGES_COMPACT:
+      return pages_workspace(op, args->n, args->n_pages, bytes);
   }
   return fail(LSA_ERR_INVALID_ARG, "unknown op %d", static_cast<int>(op));
 }
@@ -930,6 +936,9 @@ lsa_status_t lsa_device_status(lsa_stream_t stream) {
   if (v & kStatusInternal) return fail(LSA_ERR_CUDA, "a selection candidate pool bound did not hold");
   if (v & kStatusBadIndex)
     return fail(LSA_ERR_INVALID_ARG, "an attention index row held an entry >= L_max (it was skipped)");
+  if (v & kStatusBadPage)
+    return fail(LSA_ERR_INVALID_ARG, "a page, sequence or block-table entry was out of range or refused (it was skipped)");
+  if (v & kStatusNoPage) return fail(LSA_ERR_WORKSPACE, "the paged cache ran out of free pages");
   return LSA_OK;
 }
 

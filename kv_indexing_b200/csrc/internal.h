@@ -187,6 +187,99 @@ constexpr int kMaxLaunchLayers = 4;
 cudaError_t launch_attn(const AttnMaps* maps, const AttnArgs* args, int n, cudaStream_t stream);
 cudaError_t launch_attn_combine(const AttnArgs* args, int n, cudaStream_t stream);
 
+// -------------------------------------------------------------- paged cache --
+// Rows to rotate and where they go: strided rows (lsa_rope) or the slots of a
+// paged cache (lsa_pages_append; table != null).
+struct RotateArgs {
+  int B, T, H, d, offset;
+  int rot;                // rotated columns (0: copy only)
+  int interleaved, in_place;
+  float sign, amplitude;  // sign -1: the transposed rotation
+  const int* seq_len;
+  const int* q_len;       // or null
+  const void* x;
+  void* out;
+  long long xb, xt, xh;   // strides (elements)
+  long long ob, ot, oh;   // lsa_rope: strides of out; append: ob = page, ot = row stride
+  const int* table;
+  int n_pages, page_size, max_pages;
+  float* scales;          // e4m3 pool: per-token scales [n_pages, page_size]
+  int vec;                // elements per access: 16 bytes, or 1
+  int* status;
+  double freq[LSA_ROPE_MAX_PAIRS];
+};
+cudaError_t launch_rope(const RotateArgs& a, int fp32, cudaStream_t stream);
+cudaError_t launch_append(const RotateArgs& a, int e4m3, cudaStream_t stream);
+
+constexpr int kMaxLaunchPools = 32;
+constexpr int kCopyChunk = 16384;   // bytes of a page that one block moves at a time
+struct Pools {
+  uint8_t* base[kMaxLaunchPools];
+  long long stride[kMaxLaunchPools];
+  int bytes[kMaxLaunchPools];       // of a page
+  int first[kMaxLaunchPools + 1];   // first chunk of pool i among a page's chunks
+  int n;
+};
+struct PageArgs {
+  int* table;
+  int* ref;
+  int* seq_len;
+  int S, max_pages, n_pages, page_size;
+  int* status;
+};
+cudaError_t launch_reserve(const PageArgs& a, const int* len, cudaStream_t stream);
+cudaError_t launch_free(const PageArgs& a, const int* seqs, int n, cudaStream_t stream);
+cudaError_t launch_fork_plan(const PageArgs& a, const int* parent, const int* child, int n, int* plan,
+                             cudaStream_t stream);
+// rows: also the table rows, counts and lengths (once per call; pools may take several launches)
+cudaError_t launch_fork(const PageArgs& a, const int* parent, const int* child, int n, const int* plan,
+                        const Pools& pools, int rows, cudaStream_t stream);
+cudaError_t launch_copy_plan(int n_pages, const int* src, const int* dst, int n, int* ok, int* status,
+                             cudaStream_t stream);
+cudaError_t launch_copy(const Pools& pools, const int* src, const int* dst, const int* ok, int n, cudaStream_t stream);
+// ws: counters [2] (n_live, moves), then src [n_pages], dst [n_pages], map [n_pages]
+cudaError_t launch_compact_plan(const int* ref, int n_pages, int* ref_out, int* n_live, int* ws, cudaStream_t stream);
+cudaError_t launch_compact(const int* table, int S, int max_pages, int n_pages, int* table_out, const int* ws,
+                           const Pools& pools, int rows, int* status, cudaStream_t stream);
+constexpr int kCompactHeader = 64;   // ints before the lists
+
+// Attention over the paged cache. Query rows of one KV head are (token, head
+// of its group) pairs, row = t * G + head, in tiles of 128.
+struct PagedArgs {
+  int B, T, Hq, Hkv, G;
+  int n_pages, page_size, page_shift, max_pages;
+  int n_split;            // KV splits of a sequence (each takes an equal share of its blocks)
+  int n_part;             // partial results per row (1: final outputs are written directly)
+  int tiles;              // row tiles (pairs of tiles where a block takes two)
+  float scale_log2;       // scale * log2(e)
+  const int* seq_len;
+  const int* q_len;
+  const int* table;
+  const uint16_t* q;
+  uint16_t* out;          // [B, T, Hq, d_v]
+  float* lse;             // or null
+  float* part_o;          // [n_part][B * T * Hq][d_v], each normalised by its own sum
+  float* part_m;          // [n_part][B * T * Hq], log2 domain
+  float* part_l;
+  const uint8_t* kv8;     // e4m3 latent rows (else null)
+  long long kv8_page, kv8_row;
+  const float* k_scale;   // [n_pages, page_size]
+  int* status;
+};
+// K and V as (columns, slot, page) with boxes of 64 columns x box rows x 1 page.
+struct PagedMaps {
+  CUtensorMap k, v, q;
+};
+constexpr int kPagedBN = 128;      // keys per block, d = 64 / 128
+constexpr int kPagedBNMla = 64;    // keys per block, latent rows
+constexpr int kMaxParts = 128;
+cudaError_t launch_paged_attn(const PagedMaps& m, const PagedArgs& a, int d, int shared_kv, cudaStream_t stream);
+cudaError_t launch_paged_mla(const PagedMaps& m, const PagedArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_combine(const PagedArgs& a, int d_v, cudaStream_t stream);
+
+lsa_status_t paged_attn_workspace(const lsa_paged_attn_in_t* in, size_t* bytes);
+lsa_status_t pages_workspace(lsa_op_t op, int n, int n_pages, size_t* bytes);
+
 // --------------------------------------------------------------------- misc --
 int device_sm_count();
 // Records a one-line reason for lsa_last_error() and returns `st`.

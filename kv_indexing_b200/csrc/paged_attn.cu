@@ -1,0 +1,496 @@
+// Attention of new tokens over a paged cache, separate K and V, d = 64 or 128,
+// grouped heads.
+//
+//   o[r, :] = sum_{s <= pos(r)} softmax_s(scale * q[r] . K[s]) V[s]
+//
+// One pass over the keys with a running maximum and sum per row. The rows of a
+// KV head are its (token, head of the group) pairs, row = t * G + head, so any
+// group size fills the 128 rows of the score MMA.
+//
+// A block works on two row tiles in turn, so that the tensor cores compute one
+// tile's products while the other's softmax runs:
+//   SHARED = 1 (more than 128 rows): two tiles of 128 rows over the same keys;
+//   SHARED = 0 (a few rows): one tile of rows, the two halves taking the even
+//     and the odd key blocks, each with its own maximum, sum and output. The
+//     halves are merged with the KV splits.
+//
+// Threads (320): warps 0-3 and 4-7 are the softmax of the two halves, one
+// thread per row; warp 8 loads K and V pages by TMA into a ring of 128-key
+// tiles (boxes of one page, or of the page's part of the block); warp 9 issues
+// the MMAs. Scores (128 columns) and O (d columns) of both halves fill tensor
+// memory; P (bf16) overwrites the scores it came from and is the A operand of
+// the second MMA. MMAs issued by one thread run in order, so a half's next
+// scores cannot overtake the product that reads its P.
+//
+// The running maximum only moves when a block raises it by more than 2^8 (the
+// bf16 P keeps its relative precision, sums are fp32), so O is rescaled rarely.
+//
+// Keys past a row's position are masked by select. Rows of V at and past
+// seq_len (whatever a page still holds there) are cleared in shared memory
+// before the product reads them: 0 * NaN is NaN. Unmapped pages are loaded from
+// past the pool's last page, which TMA fills with zeros, and masked.
+#include "paged.cuh"
+
+namespace lsa {
+namespace {
+
+using namespace paged;
+
+constexpr int kSoft = 256;             // softmax threads
+constexpr int kThreads = 320;
+constexpr int BN = kPagedBN;
+
+template <int D, bool SHARED>
+struct Cfg {
+  static constexpr int kChunks = D / 64;
+  static constexpr int kQTile = 128 * D * 2;
+  static constexpr int kQTiles = SHARED ? 2 : 1;
+  static constexpr int kStage = BN * D * 2;
+  static constexpr int kStages = D == 128 ? (SHARED ? 5 : 6) : 10;
+  static constexpr int kOffStage = kQTiles * kQTile;
+  static constexpr int kOffMask = kOffStage + kStages * kStage;
+  static constexpr int kOffBars = kOffMask + ((kStages * 4 + 7) / 8) * 8;
+  static constexpr int kNumBars = 2 * kStages + 7;
+  static constexpr int kOffMisc = kOffBars + kNumBars * 8;
+  static constexpr size_t kSmem = 1024 + kOffMisc + 16;
+};
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 0, kColO = 256;   // S of half i at 128 i, O at 256 + D i
+
+template <int D, bool SHARED>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const PagedArgs a) {
+  using C = Cfg<D, SHARED>;
+  static_assert(C::kSmem <= 227 * 1024, "shared memory budget");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = base;
+  uint8_t* sStage = base + C::kOffStage;
+  uint32_t* mask_s = reinterpret_cast<uint32_t*>(base + C::kOffMask);   // [kStages] mapped pages of a V tile
+  uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBars);
+  uint64_t* kv_full = bars;
+  uint64_t* kv_empty = bars + C::kStages;
+  uint64_t* s_full = bars + 2 * C::kStages;   // [2]
+  uint64_t* p_full = s_full + 2;              // [2]
+  uint64_t* o_full = p_full + 2;              // [2]
+  uint64_t* q_full = o_full + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tile = a.tiles - 1 - static_cast<int>(blockIdx.x);   // the longest rows first
+  const int g = blockIdx.y;
+  const int b = blockIdx.z / a.n_split, split = blockIdx.z - b * a.n_split;
+
+  if (tid == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 128);
+      mbar_init(&o_full[i], 1);
+    }
+    mbar_init(q_full, kSoft);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tmem = *tmem_slot;
+
+  // Rows, blocks and splits of this sequence (the same in every thread).
+  const Lens L = lens_of(a, b);
+  const int rows = L.n_new * a.G;
+  const int row0 = tile * (SHARED ? 256 : 128);
+  const int first_pos = L.len - L.n_new;       // position of token t: first_pos + t
+  // keys that the last row of half i's tile sees
+  auto keys_of = [&](int i) -> int {
+    const int r0 = row0 + (SHARED ? 128 * i : 0);
+    if (r0 >= rows) return 0;
+    const int last = min(rows, r0 + 128) - 1;
+    return max(0, min(L.len, first_pos + last / a.G + 1));
+  };
+  int n0, n1, blk0 = 0;                        // steps of the halves; first key block
+  {
+    const int k0 = keys_of(0), k1 = SHARED ? keys_of(1) : k0;
+    const int all = (max(k0, k1) + BN - 1) / BN;
+    const int per = (all + a.n_split - 1) / a.n_split;
+    blk0 = split * per;
+    const int end = min(all, blk0 + per);
+    if (SHARED) {
+      n0 = max(0, min(end, (k0 + BN - 1) / BN) - blk0);
+      n1 = max(0, min(end, (k1 + BN - 1) / BN) - blk0);
+    } else {
+      const int n = max(0, end - blk0);
+      n0 = (n + 1) / 2;
+      n1 = n / 2;
+    }
+  }
+  const int n_blk = SHARED ? max(n0, n1) : n0 + n1;   // key blocks loaded
+  // ring sequence number of the K tile of half i's step s (its V tile follows)
+  auto seq_of = [&](int i, int s) -> int { return SHARED ? 2 * s : 2 * (2 * s + i); };
+
+  if (warp == 8) {
+    // ---------------------------------------------------------- producer --
+    const int per = BN >> a.page_shift;        // pages of a block (page sizes up to 128)
+    const int n_ops = C::kChunks * per;
+    const int j = lane % per, c = lane / per;
+    const int rows_box = 1 << a.page_shift;
+    const int* row = a.table + static_cast<long long>(b) * a.max_pages;
+    auto page_of = [&](int blk) -> int {       // physical page of this lane's page of the block; -1: nothing there
+      const int tok = (blk0 + blk) * BN + (j << a.page_shift);
+      if (blk >= n_blk || tok >= L.len) return -1;
+      const int p = __ldg(row + (tok >> a.page_shift));
+      if (p < 0 || p >= a.n_pages) {
+        if (c == 0) record_bad_page(a.status);
+        return -1;
+      }
+      return p;
+    };
+    int next = page_of(0);
+    bool ok = true;
+    for (int blk = 0; ok && blk < n_blk; ++blk) {
+      const int page = next;
+      next = page_of(blk + 1);
+      const uint32_t mapped = __ballot_sync(0xffffffffu, page >= 0) & ((1u << per) - 1u);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int seq = 2 * blk + kv, st = seq % C::kStages;
+        if (seq >= C::kStages) {
+          ok = __all_sync(0xffffffffu,
+                          wait(&kv_empty[st], ((seq / C::kStages) - 1) & 1, a.status, abort_flag));
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          if (kv) mask_s[st] = mapped;
+          mbar_arrive_expect_tx(&kv_full[st], C::kStage);
+        }
+        __syncwarp();
+        if (lane < n_ops)
+          tma_load_page(sStage + st * C::kStage + c * (BN * 128) + j * rows_box * 128, kv ? &tm_v : &tm_k, &kv_full[st],
+                        g * D + c * 64, 0, page >= 0 ? page : a.n_pages);
+      }
+    }
+  } else if (warp == 9) {
+    // -------------------------------------------------------- MMA issuer --
+    if (lane == 0 && n_blk > 0) {
+      const uint32_t idesc_qk = make_idesc(1, 1, 128, BN, 0, 0);
+      const uint32_t idesc_pv = make_idesc(1, 1, 128, D, 0, 1);
+      auto full = [&](int seq) { return wait(&kv_full[seq % C::kStages], (seq / C::kStages) & 1, a.status, abort_flag); };
+      auto qk = [&](int i, int s) -> bool {
+        const int seq = seq_of(i, s);
+        if (!full(seq)) return false;
+        tc_fence_after();
+        const uint32_t q0 = smem_u32(sQ) + (SHARED ? i * C::kQTile : 0);
+        const uint32_t k0 = smem_u32(sStage + (seq % C::kStages) * C::kStage);
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16(tmem + kColS + 128 * i, make_sdesc(q0 + c * 16384 + ks * 32, 16, 1024, kLayoutSW128),
+                     make_sdesc(k0 + c * (BN * 128) + ks * 32, 16, 1024, kLayoutSW128), idesc_qk, (c | ks) ? 1u : 0u);
+        umma_commit(&s_full[i]);
+        if (!SHARED || i == 1 || s >= n1) umma_commit(&kv_empty[seq % C::kStages]);
+        return true;
+      };
+      auto pv = [&](int i, int s) -> bool {
+        const int seq = seq_of(i, s) + 1;
+        if (!wait(&p_full[i], s & 1, a.status, abort_flag) || !full(seq)) return false;
+        tc_fence_after();
+        const uint32_t v0 = smem_u32(sStage + (seq % C::kStages) * C::kStage);
+#pragma unroll
+        for (int ks = 0; ks < BN / 16; ++ks)
+          umma_f16_ts(tmem + kColO + D * i, tmem + kColS + 128 * i + ks * 8,
+                      make_sdesc(v0 + ks * 2048, BN * 128, 1024, kLayoutSW128), idesc_pv, (s | ks) ? 1u : 0u);
+        if (!SHARED || i == 1 || s >= n1) umma_commit(&kv_empty[seq % C::kStages]);
+        if (s + 1 == (i ? n1 : n0)) umma_commit(&o_full[i]);
+        return true;
+      };
+      bool ok = wait(q_full, 0, a.status, abort_flag);
+      if (ok && n0 > 0) ok = qk(0, 0);
+      const int n = max(n0, n1);
+      for (int s = 0; ok && s < n; ++s) {
+        if (s < n1) ok = qk(1, s);
+        if (ok && s < n0) ok = pv(0, s);
+        if (ok && s + 1 < n0) ok = qk(0, s + 1);
+        if (ok && s < n1) ok = pv(1, s);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ----------------------------------------------------------- softmax --
+    const int half = warp >> 2;
+    const int rt = tid & 127;                   // row of the tile
+    const int r = row0 + (SHARED ? 128 * half : 0) + rt;
+    const int n_steps = half ? n1 : n0;
+    {
+      // q rows into the swizzled tiles (16-byte units, 8 to a 128-byte row)
+      const int qt = SHARED ? half : 0;
+      constexpr int U = D / 8;
+      uint8_t* dst = sQ + qt * C::kQTile;
+      const int wq = warp & 3;
+      if (SHARED || half == 0) {
+#pragma unroll 4
+        for (int i = lane; i < 32 * U; i += 32) {
+          const int rr = wq * 32 + i / U, u = i % U;
+          const int gr = row0 + (SHARED ? 128 * half : 0) + rr;
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (gr < rows) {
+            const int t = gr / a.G, h = g * a.G + gr - t * a.G;
+            v = __ldg(reinterpret_cast<const uint4*>(a.q + ((static_cast<long long>(b) * a.T + t) * a.Hq + h) * D) + u);
+          }
+          *reinterpret_cast<uint4*>(dst + (u >> 3) * 16384 + rr * 128 + (((u & 7) ^ (rr & 7)) << 4)) = v;
+        }
+        fence_proxy_async_smem();
+      }
+      mbar_arrive(q_full);
+    }
+    const int t_row = r / a.G;
+    const int bound = r < rows ? max(0, min(L.len, first_pos + t_row + 1)) : 0;   // keys this row sees
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + kColS + 128 * half + lane_base, tO = tmem + kColO + D * half + lane_base;
+    const float c = a.scale_log2;
+    float m_run = -INFINITY, l_run = 0.f;       // log2 domain
+    bool ok = true;
+    for (int s = 0; s < n_steps; ++s) {
+      const int seq_v = seq_of(half, s) + 1;
+      const int key0 = (blk0 + (SHARED ? s : 2 * s + half)) * BN;
+      ok = __all_sync(0xffffffffu, wait(&s_full[half], s & 1, a.status, abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sv[128];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * q));
+      tmem_ld_wait();
+      // the V tile's barrier also publishes the block's mapped pages
+      ok = __all_sync(0xffffffffu, wait(&kv_full[seq_v % C::kStages], (seq_v / C::kStages) & 1, a.status, abort_flag));
+      if (!ok) break;
+      const uint32_t mapped = mask_s[seq_v % C::kStages];
+      const int vis = bound - key0;             // visible columns of this block
+      const bool holes = mapped != (1u << (BN >> a.page_shift)) - 1u;
+      if (__any_sync(0xffffffffu, vis < BN) || holes) {
+#pragma unroll
+        for (int j = 0; j < BN; ++j)
+          if (j >= vis || !((mapped >> (j >> a.page_shift)) & 1u)) sv[j] = 0xFF800000u;
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < BN; j += 4)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(sv[j + e]));
+      const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+      const bool move = mb > m_run + 8.f || (m_run == -INFINITY && mb != -INFINITY);
+      float corr = 1.f;
+      if (move) {
+        corr = m_run == -INFINITY ? 0.f : ex2(m_run - mb);
+        l_run *= corr;
+        m_run = mb;
+      }
+      // this half's product of step s - 1 was issued before the scores of step s, and has completed with them
+      if (s > 0 && __any_sync(0xffffffffu, move)) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t ov[32];
+          tmem_ld32(tO + c0, ov);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * corr);
+          tmem_st32(tO + c0, ov);
+        }
+      }
+      const float mu = m_run == -INFINITY ? 0.f : m_run;   // all masked so far: exp2(-inf) = 0
+      float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float p0 = ex2(fmaf(__uint_as_float(sv[64 * q + 2 * j]), c, -mu));
+          const float p1 = ex2(fmaf(__uint_as_float(sv[64 * q + 2 * j + 1]), c, -mu));
+          ps[j & 3] += p0 + p1;
+          pk[j] = pack_bf16(p0, p1);
+        }
+        tmem_st32(tS + 32 * q, pk);
+      }
+      l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+      if (key0 + BN > L.len) {                  // the sequence's last block: nothing past its end may reach the product
+        uint8_t* vt = sStage + (seq_v % C::kStages) * C::kStage;
+        const int z0 = max(0, L.len - key0);
+        for (int i = rt; i < (BN - z0) * C::kChunks * 8; i += 128) {
+          const int row = z0 + i / (C::kChunks * 8), u = i % (C::kChunks * 8);
+          *reinterpret_cast<uint4*>(vt + (u >> 3) * (BN * 128) + row * 128 + (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&p_full[half]);
+    }
+    // ---------------------------------------------------------- epilogue --
+    const bool have = n_steps > 0;
+    if (ok && have) ok = __all_sync(0xffffffffu, wait(&o_full[half], 0, a.status, abort_flag));
+    if (ok) {
+      tc_fence_after();
+      const bool mine = r < rows;
+      const long long orow = (static_cast<long long>(b) * a.T + t_row) * a.Hq + g * a.G + (r - t_row * a.G);
+      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      const bool direct = a.n_part == 1;
+      const long long n_rows = static_cast<long long>(a.B) * a.T * a.Hq;
+      const long long prow = (SHARED ? split : 2 * split + half) * n_rows + orow;
+      if (have || direct) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t ov[32];
+          if (have) {
+            tmem_ld32(tO + c0, ov);
+            tmem_ld_wait();
+          }
+          if (!mine) continue;
+          // a row without keys is 0, whatever its accumulator holds
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            ov[i] = have && l_run > 0.f ? __float_as_uint(__uint_as_float(ov[i]) * inv) : 0u;
+          if (direct) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16(__uint_as_float(ov[8 * q + 2 * e]), __uint_as_float(ov[8 * q + 2 * e + 1]));
+              dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + c0);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dst[q] = make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+          }
+        }
+      }
+      if (mine) {
+        if (direct) {
+          if (a.lse) a.lse[orow] = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
+        } else {
+          a.part_m[prow] = m_run;
+          a.part_l[prow] = l_run;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) spin_ns(50000);   // let copies and MMAs in flight land before the exit
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D, bool SHARED>
+cudaError_t launch_t(const PagedMaps& m, const PagedArgs& a, cudaStream_t stream) {
+  using C = Cfg<D, SHARED>;
+  const void* fn = reinterpret_cast<const void*>(&paged_attn_kernel<D, SHARED>);
+  // at least half an SM's shared memory: one block per SM, as its tensor memory asks for
+  const size_t smem = C::kSmem < 120 * 1024 ? 120 * 1024 : C::kSmem;
+  const cudaError_t e = set_max_smem(fn, smem);
+  if (e != cudaSuccess) return e;
+  void* args[] = {const_cast<CUtensorMap*>(&m.k), const_cast<CUtensorMap*>(&m.v), const_cast<PagedArgs*>(&a)};
+  return launch_pdl(fn, dim3(a.tiles, a.Hkv, a.B * a.n_split), dim3(kThreads), smem, stream, args);
+}
+
+// Merges the partial results of a row: f_p = l_p 2^(m_p - m*), o = sum f_p o_p / sum f_p,
+// lse = m* + log2 sum f_p. DV / 128 (at least 1) warps a row; empty parts are
+// not read.
+template <int DV>
+__global__ void __launch_bounds__(128) paged_combine_kernel(const PagedArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int kWarps = DV >= 128 ? DV / 128 : 1;      // warps of a row
+  constexpr int kPer = DV >= 128 ? 4 : DV / 32;         // columns of a lane
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long n_rows = static_cast<long long>(a.B) * a.T * a.Hq;
+  const long long row = static_cast<long long>(blockIdx.x) * (4 / kWarps) + warp / kWarps;
+  if (row >= n_rows) return;
+  const int bt = static_cast<int>(row / a.Hq), b = bt / a.T;
+  if (bt - b * a.T >= lens_of(a, b).n_new) return;      // a padding row: left as it was
+  constexpr int kRegs = kMaxParts / 32;
+  float f[kRegs], M = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kRegs; ++i) {
+    const int p = i * 32 + lane;
+    f[i] = 0.f;
+    if (p < a.n_part) {
+      f[i] = a.part_l[p * n_rows + row];
+      if (f[i] > 0.f) M = fmaxf(M, a.part_m[p * n_rows + row]);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float den = 0.f;
+#pragma unroll
+  for (int i = 0; i < kRegs; ++i) {
+    const int p = i * 32 + lane;
+    if (f[i] > 0.f) f[i] *= exp2f(a.part_m[p * n_rows + row] - M);
+    den += f[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const int col = (warp % kWarps) * 128 + lane * kPer;
+  float acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  const float* src = a.part_o + row * DV + col;
+  struct alignas(4 * kPer) Vec { float v[kPer]; };
+#pragma unroll
+  for (int i = 0; i < kRegs; ++i) {
+    if (i * 32 >= a.n_part) break;
+    const int np = min(32, a.n_part - i * 32);
+#pragma unroll 8
+    for (int p = 0; p < np; ++p) {
+      const float w = __shfl_sync(0xffffffffu, f[i], p);
+      if (w > 0.f) {
+        const Vec o = *reinterpret_cast<const Vec*>(src + (i * 32 + p) * n_rows * DV);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] = fmaf(o.v[e], w, acc[e]);
+      }
+    }
+  }
+  uint16_t* dst = a.out + row * DV + col;
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+  if (a.lse && lane == 0 && warp % kWarps == 0)
+    a.lse[row] = den > 0.f ? (M + log2f(den)) * 0.69314718055994530942f : -INFINITY;
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attn(const PagedMaps& m, const PagedArgs& a, int d, int shared_kv, cudaStream_t stream) {
+  if (d == 128) return shared_kv ? launch_t<128, true>(m, a, stream) : launch_t<128, false>(m, a, stream);
+  return shared_kv ? launch_t<64, true>(m, a, stream) : launch_t<64, false>(m, a, stream);
+}
+
+cudaError_t launch_paged_combine(const PagedArgs& a, int d_v, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(a.B) * a.T * a.Hq;
+  const int per = d_v == 512 ? 1 : 4;
+  const void* fn = d_v == 512   ? reinterpret_cast<const void*>(&paged_combine_kernel<512>)
+                   : d_v == 128 ? reinterpret_cast<const void*>(&paged_combine_kernel<128>)
+                                : reinterpret_cast<const void*>(&paged_combine_kernel<64>);
+  void* args[] = {const_cast<PagedArgs*>(&a)};
+  return launch_pdl(fn, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(128), 0, stream, args);
+}
+
+}  // namespace lsa

@@ -16,6 +16,8 @@ constexpr unsigned long long kWaitLimitNs = 1000000000ull;  // 1 s
 constexpr int kStatusTimeout = 1;    // a kernel gave up waiting on a barrier
 constexpr int kStatusBadIndex = 2;   // an index row held an entry >= L_max (skipped)
 constexpr int kStatusInternal = 4;   // an internal capacity bound did not hold
+constexpr int kStatusBadPage = 8;    // a page, sequence or table entry was out of range (skipped)
+constexpr int kStatusNoPage = 16;    // a paged cache ran out of free pages
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -36,6 +38,13 @@ __device__ __forceinline__ void record_bad_index(int* status) {
 }
 __device__ __forceinline__ void record_internal(int* status) {
   if (status) atomicOr(status, kStatusInternal);
+}
+
+__device__ __forceinline__ void record_bad_page(int* status) {
+  if (status) atomicOr(status, kStatusBadPage);
+}
+__device__ __forceinline__ void record_no_page(int* status) {
+  if (status) atomicOr(status, kStatusNoPage);
 }
 
 // ------------------------------------------------- programmatic launch --

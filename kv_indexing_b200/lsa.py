@@ -16,15 +16,19 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "liblsa.so")
 
 LSA_OK, LSA_ERR_INVALID_ARG, LSA_ERR_UNSUPPORTED, LSA_ERR_WORKSPACE, LSA_ERR_CUDA, LSA_ERR_TIMEOUT = range(6)
-LSA_BF16, LSA_E4M3 = 0, 1
+LSA_BF16, LSA_E4M3, LSA_FP32 = 0, 1, 2
 (LSA_OP_INDEX_FLAT, LSA_OP_INDEX_HIER, LSA_OP_SELECT, LSA_OP_SPARSE_ATTN, LSA_OP_LAYER_GROUP,
- LSA_OP_INDEX_COMPRESSED) = range(6)
+ LSA_OP_INDEX_COMPRESSED, LSA_OP_PAGED_ATTN, LSA_OP_PAGES_FORK, LSA_OP_PAGES_COPY, LSA_OP_PAGES_COMPACT) = range(10)
+LSA_ROPE_SCALINGS = {"none": 0, "linear": 1, "yarn": 2}
+LSA_ROPE_MAX_PAIRS = 128
 LSA_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024   # static scratch of lsa_select_streaming_noalloc
 
 EXPORTS = [
     "lsa_status_string", "lsa_last_error", "lsa_workspace_size", "lsa_index_flat", "lsa_select_streaming",
     "lsa_pool_pages", "lsa_index_hier", "lsa_sparse_attn", "lsa_layer_group", "lsa_device_status",
     "lsa_select_streaming_noalloc", "lsa_index_compressed", "lsa_pool_pages_e4m3", "lsa_index_hier_e4m3",
+    "lsa_rope_plan", "lsa_rope", "lsa_pages_append", "lsa_paged_attn", "lsa_pages_reserve", "lsa_pages_fork",
+    "lsa_pages_free", "lsa_pages_copy", "lsa_pages_compact",
 ]
 
 
@@ -54,11 +58,44 @@ class AttnIn(ctypes.Structure):
                 ("kv_dtype", ctypes.c_int32), ("k_scale", ctypes.c_void_p)]
 
 
+class RopePlan(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_double),
+                ("freq", ctypes.c_double * LSA_ROPE_MAX_PAIRS)]
+
+
+class RopeIn(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("B", "T", "H", "d", "dtype", "offset", "inverse")] + \
+               [(f, ctypes.c_void_p) for f in ("seq_len", "q_len", "x")] + \
+               [(f, ctypes.c_int64) for f in ("x_stride_b", "x_stride_t", "x_stride_h", "out_stride_b", "out_stride_t",
+                                              "out_stride_h")]
+
+
+class AppendIn(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("B", "T", "H", "d", "n_pages", "page_size", "max_pages", "dtype",
+                                              "offset")] + \
+               [(f, ctypes.c_void_p) for f in ("seq_len", "q_len", "table", "x", "pool")] + \
+               [("page_stride", ctypes.c_int64), ("row_stride", ctypes.c_int64), ("scales", ctypes.c_void_p)]
+
+
+class PagedAttnIn(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("B", "T", "Hq", "Hkv", "d_qk", "d_v", "n_pages", "page_size",
+                                              "max_pages")] + \
+               [("scale", ctypes.c_float), ("kv_dtype", ctypes.c_int32)] + \
+               [(f, ctypes.c_void_p) for f in ("seq_len", "q_len", "table", "q", "k", "v")] + \
+               [(f, ctypes.c_int64) for f in ("k_page_stride", "k_row_stride", "v_page_stride", "v_row_stride")] + \
+               [("k_scale", ctypes.c_void_p)]
+
+
+class Pool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("page_stride", ctypes.c_int64)]
+
+
 class OpArgs(ctypes.Structure):
     _fields_ = [("indexer", ctypes.POINTER(IndexerIn)), ("attn", ctypes.POINTER(AttnIn)), ("budget", Budget),
                 ("P", ctypes.c_int32), ("M", ctypes.c_int32), ("n_layers", ctypes.c_int32),
                 ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("L_max", ctypes.c_int32),
-                ("scores_external", ctypes.c_int32), ("m", ctypes.c_int32)]
+                ("scores_external", ctypes.c_int32), ("m", ctypes.c_int32),
+                ("paged", ctypes.POINTER(PagedAttnIn)), ("n", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
 
 
 _lib = None
@@ -100,6 +137,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.lsa_layer_group.restype = i32
     lib.lsa_layer_group.argtypes = [ctypes.POINTER(IndexerIn), vp, i32, i32, Budget, i32, ctypes.POINTER(AttnIn),
                                     ctypes.POINTER(vp), ctypes.POINTER(vp), vp, vp, sz, vp]
+    f64, P = ctypes.c_double, ctypes.POINTER
+    for name, args in (
+            ("lsa_rope_plan", [i32, i32, f64, i32, f64, i32, f64, f64, f64, P(RopePlan)]),
+            ("lsa_rope", [P(RopeIn), P(RopePlan), vp, vp]),
+            ("lsa_pages_append", [P(AppendIn), P(RopePlan), vp]),
+            ("lsa_paged_attn", [P(PagedAttnIn), vp, vp, vp, sz, vp]),
+            ("lsa_pages_reserve", [vp, vp, vp, i32, i32, i32, i32, vp]),
+            ("lsa_pages_fork", [vp, vp, vp, i32, i32, i32, i32, vp, vp, i32, P(Pool), i32, vp, sz, vp]),
+            ("lsa_pages_free", [vp, vp, vp, i32, i32, i32, vp, i32, vp]),
+            ("lsa_pages_copy", [P(Pool), i32, i32, vp, vp, i32, vp, sz, vp]),
+            ("lsa_pages_compact", [vp, vp, i32, i32, i32, P(Pool), i32, vp, vp, vp, vp, sz, vp])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = i32, args
     lib.lsa_device_status.restype = i32
     lib.lsa_device_status.argtypes = [vp]
     _lib = lib
@@ -230,7 +280,8 @@ def attn_in(q, seq_len, scale, *, kv=None, k=None, v=None, d_v=None, stream_budg
 
 
 def workspace_size(op: int, *, indexer: Optional[IndexerIn] = None, attn=None, budget=(1, 0, 0), P=0, M=0,
-                   n_layers=0, B=0, T=0, L_max=0, scores_external=False, m=0) -> int:
+                   n_layers=0, B=0, T=0, L_max=0, scores_external=False, m=0, paged: Optional[PagedAttnIn] = None,
+                   n=0, n_pages=0) -> int:
     lib = load()
     a = OpArgs()
     keep = []
@@ -247,6 +298,9 @@ def workspace_size(op: int, *, indexer: Optional[IndexerIn] = None, attn=None, b
     a.P, a.M, a.n_layers, a.B, a.T, a.L_max = P, M, n_layers, B, T, L_max
     a.scores_external = int(bool(scores_external))
     a.m = m
+    if paged is not None:
+        a.paged = ctypes.pointer(paged)
+    a.n, a.n_pages = n, n_pages
     out = ctypes.c_size_t(0)
     _check(lib.lsa_workspace_size(op, ctypes.byref(a), ctypes.byref(out)))
     return out.value
@@ -489,6 +543,277 @@ def lsa_layer_group(q, w, k, seq_len, budget, layers: Sequence[dict], *, P=0, M=
     _check(lib.lsa_layer_group(ctypes.byref(ii), _ptr(page_keys), P, M, Budget(*budget), n, arr, outp, lsep,
                                _ptr(idx), _ptr(ws), _nbytes(ws), _stream(stream)))
     return idx, outs
+
+
+# ---------------------------------------------------------------------------
+# the paged cache: rotary positions, new rows, attention, page upkeep
+# ---------------------------------------------------------------------------
+
+
+def _here(t, name, dtype, dim):
+    """_need without the demand for dense rows: strides are passed on."""
+    torch = _torch()
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    cur = torch.cuda.current_device()
+    if t.device.index != cur:
+        raise ValueError(f"{name} is on {t.device}, but the calls launch on the current device cuda:{cur}")
+    dts = dtype if isinstance(dtype, tuple) else (dtype,)
+    if t.dtype not in dts:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dts}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dims")
+    return t
+
+
+def _pages_of(t, name, dtype, heads, d):
+    """(page stride, row stride) in elements of a pool [n_pages, P, heads, d] or,
+    for one head, [n_pages, P, d]: any page and row strides, dense rows."""
+    if t.dim() == 3 and heads == 1:
+        _here(t, name, dtype, 3)
+        _dims(t, name, (None, None, d))
+    else:
+        _here(t, name, dtype, 4)
+        _dims(t, name, (None, None, heads, d))
+        if heads > 1 and t.stride(2) != d:
+            raise ValueError(f"{name}: the heads of a row must be dense")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name} must have a dense last dimension")
+    P = t.shape[1]
+    row = t.stride(1) if P > 1 else heads * d
+    page = t.stride(0) if t.shape[0] > 1 else P * row
+    return page, row
+
+
+def _table(table, seq_len, q_len, B, T):
+    i32 = _torch().int32
+    _need(table, "table", i32, 2)
+    _need(seq_len, "seq_len", i32, 1)
+    _dims(table, "table", (B, None))
+    _dims(seq_len, "seq_len", (B,))
+    if q_len is not None:
+        _need(q_len, "q_len", i32, 1)
+        _dims(q_len, "q_len", (B,))
+
+
+def lsa_rope_plan(rot_dim, theta, *, interleaved=False, scaling="none", factor=1.0, orig_len=0, beta_fast=32.0,
+                  beta_slow=1.0, amplitude=0.0) -> RopePlan:
+    """Frequencies of a rotary embedding of rot_dim columns, kept by the caller and passed
+    to lsa_rope / lsa_pages_append. Pairs are (2i, 2i+1) if interleaved, else
+    (i, i + rot_dim/2). scaling: "none", "linear" or "yarn" (with orig_len); amplitude 0
+    takes the default (0.1 ln factor + 1 for yarn)."""
+    if scaling not in LSA_ROPE_SCALINGS:
+        raise ValueError(f"scaling {scaling!r} is not one of {sorted(LSA_ROPE_SCALINGS)}")
+    plan = RopePlan()
+    _check(load().lsa_rope_plan(rot_dim, int(bool(interleaved)), float(theta), LSA_ROPE_SCALINGS[scaling], float(factor),
+                                orig_len, float(beta_fast), float(beta_slow), float(amplitude), ctypes.byref(plan)))
+    return plan
+
+
+def lsa_rope(x, plan, seq_len, *, q_len=None, offset=0, inverse=False, out=None, stream=None):
+    """Rotates the columns [offset, offset + rot_dim) of x [B,T,H,d] (bf16 or fp32, any strides with
+    a dense last dimension) by each token's position; the other columns are copied. inverse: the
+    transposed rotation, which takes the gradient of the output to that of x. out may be x. Returns
+    out; rows of padding tokens of a given out are left as they were (a new out is zero there)."""
+    torch = _torch()
+    lib = load()
+    _here(x, "x", (torch.bfloat16, torch.float32), 4)
+    _need(seq_len, "seq_len", torch.int32, 1)
+    B, T, H, d = x.shape
+    _dims(seq_len, "seq_len", (B,))
+    if q_len is not None:
+        _need(q_len, "q_len", torch.int32, 1)
+        _dims(q_len, "q_len", (B,))
+    if out is None:
+        out = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+    else:
+        _here(out, "out", x.dtype, 4)
+        _dims(out, "out", tuple(x.shape))
+    if d > 1 and (x.stride(3) != 1 or out.stride(3) != 1):
+        raise ValueError("x and out must have a dense last dimension")
+    ri = RopeIn(B, T, H, d, LSA_FP32 if x.dtype == torch.float32 else LSA_BF16, offset, int(bool(inverse)),
+                _ptr(seq_len), _ptr(q_len), _ptr(x), x.stride(0), x.stride(1), x.stride(2), out.stride(0), out.stride(1),
+                out.stride(2))
+    _check(lib.lsa_rope(ctypes.byref(ri), ctypes.byref(plan), _ptr(out), _stream(stream)))
+    return out
+
+
+def lsa_pages_append(x, table, seq_len, pool, *, q_len=None, scale_pool=None, plan=None, offset=0, stream=None):
+    """Writes the new rows x [B,T,H,d] bf16 (or [B,T,d] for one head) into their pages of pool
+    [n_pages,P,H,d] (or [n_pages,P,d]): bf16, or e4m3 codes (torch.float8_e4m3fn) with the row's
+    scale in scale_pool [n_pages,P] fp32. plan: every head's columns [offset, offset + rot_dim) are
+    rotated first. seq_len counts the new tokens. Returns pool."""
+    torch = _torch()
+    lib = load()
+    if x is not None and x.dim() == 3:
+        _need(x, "x", torch.bfloat16, 3)
+        B, T, d = x.shape
+        H = 1
+    else:
+        _need(x, "x", torch.bfloat16, 4)
+        B, T, H, d = x.shape
+    _table(table, seq_len, q_len, B, T)
+    page, row = _pages_of(pool, "pool", (torch.bfloat16, torch.float8_e4m3fn), H, d)
+    e4m3 = pool.dtype == torch.float8_e4m3fn
+    if e4m3:
+        _need(scale_pool, "scale_pool", torch.float32, 2)
+        _dims(scale_pool, "scale_pool", tuple(pool.shape[:2]))
+    elif scale_pool is not None:
+        raise ValueError("scale_pool is for an e4m3 pool only")
+    ai = AppendIn(B, T, H, d, pool.shape[0], pool.shape[1], table.shape[1], LSA_E4M3 if e4m3 else LSA_BF16, offset,
+                  _ptr(seq_len), _ptr(q_len), _ptr(table), _ptr(x), _ptr(pool), page, row, _ptr(scale_pool))
+    _check(lib.lsa_pages_append(ctypes.byref(ai), ctypes.byref(plan) if plan is not None else None, _stream(stream)))
+    return pool
+
+
+def paged_attn_in(q, table, seq_len, scale, *, kv=None, k=None, v=None, d_v=None, kv_scale=None,
+                  q_len=None) -> PagedAttnIn:
+    """Describe paged attention: q [B,T,Hq,d_qk] bf16; latent rows kv [n_pages,P,576] (bf16, or
+    torch.float8_e4m3fn with kv_scale [n_pages,P]), or k, v [n_pages,P,Hkv,d] bf16."""
+    torch = _torch()
+    _need(q, "q", torch.bfloat16, 4)
+    B, T, Hq, d_qk = q.shape
+    _table(table, seq_len, q_len, B, T)
+    if kv is not None:
+        if k is not None or v is not None:
+            raise ValueError("give kv (latent rows) or k and v, not both")
+        page, row = _pages_of(kv, "kv", (torch.bfloat16, torch.float8_e4m3fn), 1, d_qk)
+        e4m3 = kv.dtype == torch.float8_e4m3fn
+        if e4m3:
+            _need(kv_scale, "kv_scale", torch.float32, 2)
+            _dims(kv_scale, "kv_scale", tuple(kv.shape[:2]))
+        elif kv_scale is not None:
+            raise ValueError("kv_scale is for an e4m3 kv only")
+        return PagedAttnIn(B, T, Hq, 1, d_qk, d_v if d_v is not None else 512, kv.shape[0], kv.shape[1], table.shape[1],
+                           float(scale), LSA_E4M3 if e4m3 else LSA_BF16, _ptr(seq_len), _ptr(q_len), _ptr(table), _ptr(q),
+                           _ptr(kv), _ptr(kv), page, row, page, row, _ptr(kv_scale))
+    if kv_scale is not None:
+        raise ValueError("kv_scale is for an e4m3 kv only")
+    _here(k, "k", torch.bfloat16, 4)
+    Hkv = k.shape[2]
+    kp, kr = _pages_of(k, "k", torch.bfloat16, Hkv, d_qk)
+    _here(v, "v", torch.bfloat16, 4)
+    vp, vr = _pages_of(v, "v", torch.bfloat16, Hkv, v.shape[3])
+    _dims(v, "v", (k.shape[0], k.shape[1], Hkv, d_v))
+    return PagedAttnIn(B, T, Hq, Hkv, d_qk, v.shape[3], k.shape[0], k.shape[1], table.shape[1], float(scale), LSA_BF16,
+                       _ptr(seq_len), _ptr(q_len), _ptr(table), _ptr(q), _ptr(k), _ptr(v), kp, kr, vp, vr, None)
+
+
+def lsa_paged_attn(q, table, seq_len, scale, *, kv=None, k=None, v=None, d_v=None, kv_scale=None, q_len=None, out=None,
+                   lse=None, workspace=None, stream=None):
+    """Attention of the new tokens q [B,T,Hq,d_qk] over every cached token they see (causal; seq_len
+    counts the new tokens). The cache is kv (latent rows, MLA) or k and v, in pages listed by table
+    [B,max_pages]. Returns (out [B,T,Hq,d_v] bf16, lse or None); rows t >= q_len[b] of a given out
+    are left as they were (a new out is zero there)."""
+    torch = _torch()
+    lib = load()
+    pi = paged_attn_in(q, table, seq_len, scale, kv=kv, k=k, v=v, d_v=d_v, kv_scale=kv_scale, q_len=q_len)
+    shape = (pi.B, pi.T, pi.Hq, pi.d_v)
+    if out is None:
+        make = torch.empty if q_len is None else torch.zeros
+        out = make(shape, dtype=torch.bfloat16, device=q.device)
+    _out(out, "out", torch.bfloat16, shape)
+    _out(lse, "lse", torch.float32, shape[:3])
+    ws = _workspace(workspace_size(LSA_OP_PAGED_ATTN, paged=pi), q.device, workspace)
+    _check(lib.lsa_paged_attn(ctypes.byref(pi), _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+    return out, lse
+
+
+def _cache(table, ref, seq_len=None):
+    """(S, max_pages, n_pages) of a table [S,max_pages] and counts ref [n_pages], all int32."""
+    i32 = _torch().int32
+    _need(table, "table", i32, 2)
+    _need(ref, "ref", i32, 1)
+    if seq_len is not None:
+        _need(seq_len, "seq_len", i32, 1)
+        _dims(seq_len, "seq_len", (table.shape[0],))
+    return table.shape[0], table.shape[1], ref.shape[0]
+
+
+def _list(t, name, n=None):
+    i32 = _torch().int32
+    _need(t, name, i32, 1)
+    if n is not None:
+        _dims(t, name, (n,))
+    return t.shape[0]
+
+
+def _pools(pools, n_pages):
+    """Descriptors of pools [n_pages, ...]: any page stride, dense pages of a multiple of 16 bytes."""
+    cur = _torch().cuda.current_device()
+    arr = (Pool * max(1, len(pools)))()
+    for i, t in enumerate(pools):
+        if not t.is_cuda or t.device.index != cur:
+            raise ValueError(f"pools[{i}] must be a CUDA tensor on the current device cuda:{cur}")
+        if t.dim() < 2 or t.shape[0] != n_pages:
+            raise ValueError(f"pools[{i}] has shape {tuple(t.shape)}, expected ({n_pages}, ...)")
+        if not t[0].is_contiguous():
+            raise ValueError(f"pools[{i}]: a page must be contiguous")
+        es = t.element_size()
+        page = t[0].numel() * es
+        arr[i] = Pool(t.data_ptr(), page, t.stride(0) * es if n_pages > 1 else page)
+    return arr
+
+
+def lsa_pages_reserve(table, ref, lens, page_size, *, stream=None):
+    """Maps pages (the lowest free ones) until row s of table [S,max_pages] holds lens[s] tokens."""
+    S, max_pages, n_pages = _cache(table, ref)
+    _list(lens, "lens", S)
+    _check(load().lsa_pages_reserve(_ptr(table), _ptr(ref), _ptr(lens), S, max_pages, n_pages, page_size,
+                                    _stream(stream)))
+
+
+def lsa_pages_free(table, ref, seq_len, seqs, *, stream=None):
+    """Frees the sequences seqs [n]: their pages' counts - 1, rows unmapped, lengths 0."""
+    S, max_pages, n_pages = _cache(table, ref, seq_len)
+    n = _list(seqs, "seqs")
+    _check(load().lsa_pages_free(_ptr(table), _ptr(ref), _ptr(seq_len), S, max_pages, n_pages, _ptr(seqs), n,
+                                 _stream(stream)))
+
+
+def lsa_pages_fork(table, ref, seq_len, page_size, parent, child, pools: Sequence, *, workspace=None, stream=None):
+    """Makes sequences child[i] copies of parent[i]: full pages shared, a partly filled last page
+    copied in every pool. Children must be free (lsa_pages_free)."""
+    S, max_pages, n_pages = _cache(table, ref, seq_len)
+    n = _list(parent, "parent")
+    _list(child, "child", n)
+    arr = _pools(pools, n_pages)
+    ws = _workspace(workspace_size(LSA_OP_PAGES_FORK, n=n), table.device, workspace)
+    _check(load().lsa_pages_fork(_ptr(table), _ptr(ref), _ptr(seq_len), S, max_pages, n_pages, page_size, _ptr(parent),
+                                 _ptr(child), n, arr, len(pools), _ptr(ws), _nbytes(ws), _stream(stream)))
+
+
+def lsa_pages_copy(pools: Sequence, src, dst, *, workspace=None, stream=None):
+    """Copies page src[i] to dst[i] in every pool [n_pages, ...]."""
+    if not len(pools):
+        raise ValueError("need at least one pool")
+    n_pages = pools[0].shape[0]
+    n = _list(src, "src")
+    _list(dst, "dst", n)
+    arr = _pools(pools, n_pages)
+    ws = _workspace(workspace_size(LSA_OP_PAGES_COPY, n=n), src.device, workspace)
+    _check(load().lsa_pages_copy(arr, len(pools), n_pages, _ptr(src), _ptr(dst), n, _ptr(ws), _nbytes(ws),
+                                 _stream(stream)))
+
+
+def lsa_pages_compact(table, ref, pools: Sequence, *, table_out=None, ref_out=None, n_live=None, workspace=None,
+                      stream=None):
+    """Packs the live pages into the first n_live pages of every pool. table_out and ref_out default to
+    table and ref themselves. Returns (table_out, ref_out, n_live [1] int32)."""
+    torch = _torch()
+    S, max_pages, n_pages = _cache(table, ref)
+    table_out = table if table_out is None else _out(table_out, "table_out", torch.int32, (S, max_pages))
+    ref_out = ref if ref_out is None else _out(ref_out, "ref_out", torch.int32, (n_pages,))
+    if n_live is None:
+        n_live = torch.empty(1, dtype=torch.int32, device=table.device)
+    _out(n_live, "n_live", torch.int32, (1,))
+    arr = _pools(pools, n_pages)
+    ws = _workspace(workspace_size(LSA_OP_PAGES_COMPACT, n_pages=n_pages), table.device, workspace)
+    _check(load().lsa_pages_compact(_ptr(table), _ptr(ref), S, max_pages, n_pages, arr, len(pools), _ptr(table_out),
+                                    _ptr(ref_out), _ptr(n_live), _ptr(ws), _nbytes(ws), _stream(stream)))
+    return table_out, ref_out, n_live
 
 
 def lsa_device_status(stream=None) -> int:
