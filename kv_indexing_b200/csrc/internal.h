@@ -244,13 +244,13 @@ cudaError_t launch_compact(const int* table, int S, int max_pages, int n_pages, 
 constexpr int kCompactHeader = 64;   // ints before the lists
 
 // Attention over the paged cache. Query rows of one KV head are (token, head
-// of its group) pairs, row = t * G + head, in tiles of 128.
+// of its group) pairs, row = t * G + head, in tiles of tile_rows.
 struct PagedArgs {
   int B, T, Hq, Hkv, G;
-  int n_pages, page_size, page_shift, max_pages;
-  int n_split;            // KV splits of a sequence (each takes an equal share of its blocks)
-  int n_part;             // partial results per row (1: final outputs are written directly)
-  int tiles;              // row tiles (pairs of tiles where a block takes two)
+  int n_pages, page_shift, max_pages;
+  int tiles;              // row tiles of a (sequence, KV head)
+  int tile_rows;
+  int workers;            // parts that the list of key blocks is cut into
   float scale_log2;       // scale * log2(e)
   const int* seq_len;
   const int* q_len;
@@ -258,8 +258,11 @@ struct PagedArgs {
   const uint16_t* q;
   uint16_t* out;          // [B, T, Hq, d_v]
   float* lse;             // or null
-  float* part_o;          // [n_part][B * T * Hq][d_v], each normalised by its own sum
-  float* part_m;          // [n_part][B * T * Hq], log2 domain
+  // for the merge of tiles that are cut
+  long long* head;        // list length, workers in use
+  longlong2* span;        // [Hkv * B * tiles]: first block in the list, number of blocks
+  float* part_o;          // [2 * workers][tile_rows][d_v], each normalised by its own sum
+  float* part_m;          // [2 * workers][tile_rows], log2 domain
   float* part_l;
   const uint8_t* kv8;     // e4m3 latent rows (else null)
   long long kv8_page, kv8_row;
@@ -268,11 +271,11 @@ struct PagedArgs {
 };
 // K and V as (columns, slot, page) with boxes of 64 columns x box rows x 1 page.
 struct PagedMaps {
-  CUtensorMap k, v, q;
+  CUtensorMap k, v;
 };
-constexpr int kPagedBN = 128;      // keys per block, d = 64 / 128
-constexpr int kPagedBNMla = 64;    // keys per block, latent rows
-constexpr int kMaxParts = 128;
+constexpr int kPagedBN = 128;      // keys per block
+constexpr int kPagedBox = 64;      // most rows of a box, latent rows
+constexpr int kMaxWorkers = 160;   // a merge keeps one weight per worker
 cudaError_t launch_paged_attn(const PagedMaps& m, const PagedArgs& a, int d, int shared_kv, cudaStream_t stream);
 cudaError_t launch_paged_mla(const PagedMaps& m, const PagedArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_combine(const PagedArgs& a, int d_v, cudaStream_t stream);

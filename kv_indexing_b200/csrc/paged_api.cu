@@ -130,41 +130,39 @@ lsa_status_t check_paged(const lsa_paged_attn_in_t* in) {
 }
 
 struct PagedPlan {
-  int shared_kv, tiles, n_split, n_part;
+  int shared_kv, tile_rows, tiles, workers;
 };
 
+// Latent rows: tiles of 128 rows, a worker is a pair of SMs. Else tiles of 256
+// rows (two halves over the same keys) where a KV head has more than 128, and
+// one tile (two halves over alternate keys) where it has fewer; a worker is an
+// SM.
 PagedPlan paged_plan(const lsa_paged_attn_in_t* in) {
   PagedPlan p{};
-  const int sms = device_sm_count();
-  const long long cap = static_cast<long long>(in->max_pages) * in->page_size;
-  if (is_mla(in)) {
-    const long long rows = static_cast<long long>(in->T) * in->Hq;
-    p.tiles = static_cast<int>((rows + 127) / 128);
-    const long long items = static_cast<long long>(in->B) * p.tiles;
-    const long long blocks = (cap + kPagedBNMla - 1) / kPagedBNMla;
-    long long ns = (sms / 2) / items;
-    ns = std::max(1ll, std::min({ns, blocks, static_cast<long long>(kMaxParts)}));
-    p.n_split = p.n_part = static_cast<int>(ns);
-    return p;
-  }
+  const bool mla = is_mla(in);
   const long long rows = static_cast<long long>(in->T) * (in->Hq / in->Hkv);
-  p.shared_kv = rows > 128;
-  const int per = p.shared_kv ? 256 : 128;
-  p.tiles = static_cast<int>((rows + per - 1) / per);
-  const long long items = static_cast<long long>(in->B) * in->Hkv * p.tiles;
-  const long long blocks = (cap + kPagedBN - 1) / kPagedBN;
-  long long ns = sms / items;
-  const long long most = p.shared_kv ? blocks : (blocks + 1) / 2;
-  ns = std::max(1ll, std::min({ns, most, static_cast<long long>(kMaxParts / 2)}));
-  p.n_split = static_cast<int>(ns);
-  p.n_part = p.shared_kv ? p.n_split : 2 * p.n_split;
+  p.shared_kv = !mla && rows > 128;
+  p.tile_rows = p.shared_kv ? 256 : 128;
+  p.tiles = static_cast<int>((rows + p.tile_rows - 1) / p.tile_rows);
+  const int sms = device_sm_count();
+  const long long blocks = (static_cast<long long>(in->max_pages) * in->page_size + kPagedBN - 1) / kPagedBN;
+  const long long most = static_cast<long long>(in->B) * in->Hkv * p.tiles * blocks;
+  p.workers = static_cast<int>(std::min({static_cast<long long>(mla ? sms / 2 : sms), most, static_cast<long long>(kMaxWorkers)}));
   return p;
 }
 
-size_t paged_ws(const lsa_paged_attn_in_t* in, const PagedPlan& p) {
-  if (p.n_part == 1) return 0;
-  const size_t n = static_cast<size_t>(p.n_part) * in->B * in->T * in->Hq;
-  return up256(n * in->d_v * 4) + 2 * up256(n * 4);
+struct PagedLayout {
+  size_t span, o, m, l, total;
+};
+PagedLayout paged_ws(const lsa_paged_attn_in_t* in, const PagedPlan& p) {
+  PagedLayout w;
+  const size_t rows = 2 * static_cast<size_t>(p.workers) * p.tile_rows;
+  w.span = 256;
+  w.o = w.span + up256(static_cast<size_t>(in->Hkv) * in->B * p.tiles * sizeof(longlong2));
+  w.m = w.o + up256(rows * in->d_v * 4);
+  w.l = w.m + up256(rows * 4);
+  w.total = w.l + up256(rows * 4);
+  return w;
 }
 
 lsa_status_t check_pools(const lsa_pool_t* pools, int n_pools) {
@@ -226,7 +224,7 @@ size_t compact_ws(int n_pages) { return up256((kCompactHeader + 3 * static_cast<
 lsa_status_t paged_attn_workspace(const lsa_paged_attn_in_t* in, size_t* bytes) {
   const lsa_status_t s = check_paged(in);
   if (s != LSA_OK) return s;
-  *bytes = paged_ws(in, paged_plan(in));
+  *bytes = paged_ws(in, paged_plan(in)).total;
   return LSA_OK;
 }
 
@@ -384,27 +382,25 @@ lsa_status_t lsa_paged_attn(const lsa_paged_attn_in_t* in, void* out, float* lse
   if (!aligned(out, 16) || (lse && !aligned(lse, 4)))
     return set_error(LSA_ERR_INVALID_ARG, "out must be 16-byte aligned");
   const PagedPlan p = paged_plan(in);
-  if ((s = check_space(workspace, workspace_bytes, paged_ws(in, p))) != LSA_OK) return s;
+  const PagedLayout lay = paged_ws(in, p);
+  if ((s = check_space(workspace, workspace_bytes, lay.total)) != LSA_OK) return s;
   PagedArgs a{};
   a.B = in->B; a.T = in->T; a.Hq = in->Hq; a.Hkv = in->Hkv; a.G = in->Hq / in->Hkv;
-  a.n_pages = in->n_pages; a.page_size = in->page_size; a.max_pages = in->max_pages;
+  a.n_pages = in->n_pages; a.max_pages = in->max_pages;
   while ((1 << a.page_shift) < in->page_size) ++a.page_shift;
-  a.n_split = p.n_split; a.n_part = p.n_part; a.tiles = p.tiles;
+  a.tiles = p.tiles; a.tile_rows = p.tile_rows; a.workers = p.workers;
   a.scale_log2 = in->scale * 1.4426950408889634f;
   a.seq_len = in->seq_len; a.q_len = in->q_len; a.table = in->table;
   a.q = static_cast<const uint16_t*>(in->q);
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = device_status_ptr();
-  if (p.n_part > 1) {
-    const size_t n = static_cast<size_t>(p.n_part) * in->B * in->T * in->Hq;
-    uint8_t* w = static_cast<uint8_t*>(workspace);
-    a.part_o = reinterpret_cast<float*>(w);
-    w += up256(n * in->d_v * 4);
-    a.part_m = reinterpret_cast<float*>(w);
-    w += up256(n * 4);
-    a.part_l = reinterpret_cast<float*>(w);
-  }
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.head = reinterpret_cast<long long*>(w);
+  a.span = reinterpret_cast<longlong2*>(w + lay.span);
+  a.part_o = reinterpret_cast<float*>(w + lay.o);
+  a.part_m = reinterpret_cast<float*>(w + lay.m);
+  a.part_l = reinterpret_cast<float*>(w + lay.l);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   PagedMaps m{};
   if (is_mla(in)) {
@@ -413,7 +409,7 @@ lsa_status_t lsa_paged_attn(const lsa_paged_attn_in_t* in, void* out, float* lse
       a.kv8_page = in->k_page_stride; a.kv8_row = in->k_row_stride;
       a.k_scale = in->k_scale;
     } else if ((s = page_map(&m.k, in->k, 576, in->page_size, in->n_pages, in->k_row_stride, in->k_page_stride,
-                             std::min(in->page_size, kPagedBNMla))) != LSA_OK) {
+                             std::min(in->page_size, kPagedBox))) != LSA_OK) {
       return s;
     }
     s = cuda_check(launch_paged_mla(m, a, st), "paged latent attention launch");
@@ -427,7 +423,7 @@ lsa_status_t lsa_paged_attn(const lsa_paged_attn_in_t* in, void* out, float* lse
       return s;
     s = cuda_check(launch_paged_attn(m, a, in->d_qk, p.shared_kv, st), "paged attention launch");
   }
-  if (s != LSA_OK || p.n_part == 1) return s;
+  if (s != LSA_OK) return s;
   return cuda_check(launch_paged_combine(a, in->d_v, st), "paged combine launch");
 }
 

@@ -11,8 +11,10 @@
 // tile's products while the other's softmax runs:
 //   SHARED = 1 (more than 128 rows): two tiles of 128 rows over the same keys;
 //   SHARED = 0 (a few rows): one tile of rows, the two halves taking the even
-//     and the odd key blocks, each with its own maximum, sum and output. The
-//     halves are merged with the KV splits.
+//     and the odd key blocks of a piece, each with its own maximum, sum and
+//     output; half 1 hands its output to half 0 through shared memory.
+//
+// A block works through the pieces of the work list (paged.cuh) that are its.
 //
 // Threads (320): warps 0-3 and 4-7 are the softmax of the two halves, one
 // thread per row; warp 8 loads K and V pages by TMA into a ring of 128-key
@@ -46,12 +48,15 @@ struct Cfg {
   static constexpr int kQTile = 128 * D * 2;
   static constexpr int kQTiles = SHARED ? 2 : 1;
   static constexpr int kStage = BN * D * 2;
-  static constexpr int kStages = D == 128 ? (SHARED ? 5 : 6) : 10;
+  static constexpr int kStages = D == 128 ? 5 : 10;
   static constexpr int kOffStage = kQTiles * kQTile;
   static constexpr int kOffMask = kOffStage + kStages * kStage;
   static constexpr int kOffBars = kOffMask + ((kStages * 4 + 7) / 8) * 8;
-  static constexpr int kNumBars = 2 * kStages + 7;
-  static constexpr int kOffMisc = kOffBars + kNumBars * 8;
+  static constexpr int kNumBars = 2 * kStages + 9;
+  static constexpr int kOffWork = kOffBars + kNumBars * 8;
+  static constexpr int kOffMerge = (kOffWork + 9 * static_cast<int>(sizeof(Work)) + 15) / 16 * 16;   // the block's, and the softmax warps'
+  static constexpr int kMergeRow = 36;                 // floats: 32 columns, padded
+  static constexpr int kOffMisc = kOffMerge + (SHARED ? 0 : 128 * kMergeRow * 4);
   static constexpr size_t kSmem = 1024 + kOffMisc + 16;
 };
 constexpr uint32_t kTmemCols = 512;
@@ -75,13 +80,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_full = s_full + 2;              // [2]
   uint64_t* o_full = p_full + 2;              // [2]
   uint64_t* q_full = o_full + 2;
+  uint64_t* mg_full = q_full + 1;             // half 1's columns are in the merge buffer / have been read
+  uint64_t* mg_empty = mg_full + 1;
+  float* merge_s = reinterpret_cast<float*>(base + C::kOffMerge);
+  Work* work_s = reinterpret_cast<Work*>(base + C::kOffWork);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int tile = a.tiles - 1 - static_cast<int>(blockIdx.x);   // the longest rows first
-  const int g = blockIdx.y;
-  const int b = blockIdx.z / a.n_split, split = blockIdx.z - b * a.n_split;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  constexpr int kTile = SHARED ? 256 : 128;
+  const int worker = blockIdx.x;
 
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -94,6 +103,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&o_full[i], 1);
     }
     mbar_init(q_full, kSoft);
+    mbar_init(mg_full, 128);
+    mbar_init(mg_empty, 128);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -101,43 +112,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 0) {
+    const Work k = plan_work<kTile, BN>(a, worker, a.workers);
+    if (lane == 0) *work_s = k;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();
-  pdl_trigger();
   const uint32_t tmem = *tmem_slot;
+  bool ok = true;
 
-  // Rows, blocks and splits of this sequence (the same in every thread).
-  const Lens L = lens_of(a, b);
-  const int rows = L.n_new * a.G;
-  const int row0 = tile * (SHARED ? 256 : 128);
-  const int first_pos = L.len - L.n_new;       // position of token t: first_pos + t
-  // keys that the last row of half i's tile sees
-  auto keys_of = [&](int i) -> int {
-    const int r0 = row0 + (SHARED ? 128 * i : 0);
-    if (r0 >= rows) return 0;
-    const int last = min(rows, r0 + 128) - 1;
-    return max(0, min(L.len, first_pos + last / a.G + 1));
+  // A piece: its sequence, rows, and the steps of the halves (the same in every thread).
+  struct Piece {
+    int b, g, row0, rows, first_pos, len;
+    int n0, n1;                                // steps of the halves
   };
-  int n0, n1, blk0 = 0;                        // steps of the halves; first key block
-  {
-    const int k0 = keys_of(0), k1 = SHARED ? keys_of(1) : k0;
-    const int all = (max(k0, k1) + BN - 1) / BN;
-    const int per = (all + a.n_split - 1) / a.n_split;
-    blk0 = split * per;
-    const int end = min(all, blk0 + per);
+  auto piece_of = [&](const Work& k) -> Piece {
+    Piece p;
+    p.b = k.bt / a.tiles;
+    p.g = k.g;
+    p.row0 = (k.bt - p.b * a.tiles) * kTile;
+    const Lens L = lens_of(a, p.b);
+    p.len = L.len;
+    p.rows = L.n_new * a.G;
+    p.first_pos = L.len - L.n_new;             // position of token t: first_pos + t
     if (SHARED) {
-      n0 = max(0, min(end, (k0 + BN - 1) / BN) - blk0);
-      n1 = max(0, min(end, (k1 + BN - 1) / BN) - blk0);
+      // key blocks that the last row of half i's tile sees
+      auto blocks = [&](int r0) -> int {
+        if (r0 >= p.rows) return 0;
+        return (max(0, min(L.len, p.first_pos + (min(p.rows, r0 + 128) - 1) / a.G + 1)) + BN - 1) / BN;
+      };
+      const int end = k.blk0 + k.n;
+      p.n0 = max(0, min(end, blocks(p.row0)) - k.blk0);
+      p.n1 = max(0, min(end, blocks(p.row0 + 128)) - k.blk0);
     } else {
-      const int n = max(0, end - blk0);
-      n0 = (n + 1) / 2;
-      n1 = n / 2;
+      p.n0 = (k.n + 1) / 2;
+      p.n1 = k.n / 2;
     }
-  }
-  const int n_blk = SHARED ? max(n0, n1) : n0 + n1;   // key blocks loaded
-  // ring sequence number of the K tile of half i's step s (its V tile follows)
+    return p;
+  };
+  // key blocks that are loaded
+  auto n_blk_of = [&](const Piece& p) -> int { return SHARED ? max(p.n0, p.n1) : p.n0 + p.n1; };
+  // place in the ring, from the piece's first tile on, of the K tile of half i's step s (its V tile follows)
   auto seq_of = [&](int i, int s) -> int { return SHARED ? 2 * s : 2 * (2 * s + i); };
 
   if (warp == 8) {
@@ -146,77 +164,87 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int n_ops = C::kChunks * per;
     const int j = lane % per, c = lane / per;
     const int rows_box = 1 << a.page_shift;
-    const int* row = a.table + static_cast<long long>(b) * a.max_pages;
-    auto page_of = [&](int blk) -> int {       // physical page of this lane's page of the block; -1: nothing there
-      const int tok = (blk0 + blk) * BN + (j << a.page_shift);
-      if (blk >= n_blk || tok >= L.len) return -1;
-      const int p = __ldg(row + (tok >> a.page_shift));
-      if (p < 0 || p >= a.n_pages) {
-        if (c == 0) record_bad_page(a.status);
-        return -1;
-      }
-      return p;
-    };
-    int next = page_of(0);
-    bool ok = true;
-    for (int blk = 0; ok && blk < n_blk; ++blk) {
-      const int page = next;
-      next = page_of(blk + 1);
-      const uint32_t mapped = __ballot_sync(0xffffffffu, page >= 0) & ((1u << per) - 1u);
+    uint32_t seq = 0;
+    for (Work k = *work_s; ok && k.n > 0; next_work<kTile, BN>(a, k)) {
+      const Piece p = piece_of(k);
+      const int n_blk = n_blk_of(p);
+      const int* row = a.table + static_cast<long long>(p.b) * a.max_pages;
+      auto page_of = [&](int blk) -> int {     // physical page of this lane's page of the block; -1: nothing there
+        const int tok = (k.blk0 + blk) * BN + (j << a.page_shift);
+        if (blk >= n_blk || tok >= p.len) return -1;
+        const int pg = __ldg(row + (tok >> a.page_shift));
+        if (pg < 0 || pg >= a.n_pages) {
+          if (c == 0) record_bad_page(a.status);
+          return -1;
+        }
+        return pg;
+      };
+      int next = page_of(0);
+      for (int blk = 0; ok && blk < n_blk; ++blk) {
+        const int page = next;
+        next = page_of(blk + 1);
+        const uint32_t mapped = __ballot_sync(0xffffffffu, page >= 0) & ((1u << per) - 1u);
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int seq = 2 * blk + kv, st = seq % C::kStages;
-        if (seq >= C::kStages) {
-          ok = __all_sync(0xffffffffu,
-                          wait(&kv_empty[st], ((seq / C::kStages) - 1) & 1, a.status, abort_flag));
+        for (int kv = 0; kv < 2; ++kv, ++seq) {
+          const uint32_t st = seq % C::kStages;
+          ok = __all_sync(0xffffffffu, wait(&kv_empty[st], ((seq / C::kStages) & 1) ^ 1, a.status, abort_flag));
           if (!ok) break;
+          if (lane == 0) {
+            if (kv) mask_s[st] = mapped;
+            mbar_arrive_expect_tx(&kv_full[st], C::kStage);
+          }
+          __syncwarp();
+          if (lane < n_ops)
+            tma_load_page(sStage + st * C::kStage + c * (BN * 128) + j * rows_box * 128, kv ? &tm_v : &tm_k, &kv_full[st],
+                          p.g * D + c * 64, 0, page >= 0 ? page : a.n_pages);
         }
-        if (lane == 0) {
-          if (kv) mask_s[st] = mapped;
-          mbar_arrive_expect_tx(&kv_full[st], C::kStage);
-        }
-        __syncwarp();
-        if (lane < n_ops)
-          tma_load_page(sStage + st * C::kStage + c * (BN * 128) + j * rows_box * 128, kv ? &tm_v : &tm_k, &kv_full[st],
-                        g * D + c * 64, 0, page >= 0 ? page : a.n_pages);
       }
     }
   } else if (warp == 9) {
     // -------------------------------------------------------- MMA issuer --
-    if (lane == 0 && n_blk > 0) {
-      const uint32_t idesc_qk = make_idesc(1, 1, 128, BN, 0, 0);
-      const uint32_t idesc_pv = make_idesc(1, 1, 128, D, 0, 1);
-      auto full = [&](int seq) { return wait(&kv_full[seq % C::kStages], (seq / C::kStages) & 1, a.status, abort_flag); };
+    const uint32_t idesc_qk = make_idesc(1, 1, 128, BN, 0, 0);
+    const uint32_t idesc_pv = make_idesc(1, 1, 128, D, 0, 1);
+    const uint64_t dQ = make_sdesc(smem_u32(sQ), 16, 1024, kLayoutSW128);
+    const uint64_t dK = make_sdesc(smem_u32(sStage), 16, 1024, kLayoutSW128);
+    const uint64_t dV = make_sdesc(smem_u32(sStage), BN * 128, 1024, kLayoutSW128);
+    uint32_t seq0 = 0, seg = 0, done0 = 0, done1 = 0;        // ring places, pieces, steps of the halves before this piece
+    for (Work k = *work_s; ok && k.n > 0; next_work<kTile, BN>(a, k), ++seg) {
+      const Piece p = piece_of(k);
+      const int n0 = p.n0, n1 = p.n1;
+      auto full = [&](uint32_t seq) { return wait(&kv_full[seq % C::kStages], (seq / C::kStages) & 1, a.status, abort_flag); };
       auto qk = [&](int i, int s) -> bool {
-        const int seq = seq_of(i, s);
+        const uint32_t seq = seq0 + seq_of(i, s), st = seq % C::kStages;
         if (!full(seq)) return false;
         tc_fence_after();
-        const uint32_t q0 = smem_u32(sQ) + (SHARED ? i * C::kQTile : 0);
-        const uint32_t k0 = smem_u32(sStage + (seq % C::kStages) * C::kStage);
+        if (elect_one()) {
+          const uint64_t q0 = dQ + (SHARED ? i * (C::kQTile / 16) : 0), k0 = dK + st * (C::kStage / 16);
 #pragma unroll
-        for (int c = 0; c < C::kChunks; ++c)
+          for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_f16(tmem + kColS + 128 * i, make_sdesc(q0 + c * 16384 + ks * 32, 16, 1024, kLayoutSW128),
-                     make_sdesc(k0 + c * (BN * 128) + ks * 32, 16, 1024, kLayoutSW128), idesc_qk, (c | ks) ? 1u : 0u);
-        umma_commit(&s_full[i]);
-        if (!SHARED || i == 1 || s >= n1) umma_commit(&kv_empty[seq % C::kStages]);
+            for (int ks = 0; ks < 4; ++ks)
+              umma_f16(tmem + kColS + 128 * i, q0 + c * 1024 + ks * 2, k0 + c * (BN * 8) + ks * 2, idesc_qk, (c | ks) ? 1u : 0u);
+          umma_commit(&s_full[i]);
+          if (!SHARED || i == 1 || s >= n1) umma_commit(&kv_empty[st]);
+        }
+        __syncwarp();
         return true;
       };
       auto pv = [&](int i, int s) -> bool {
-        const int seq = seq_of(i, s) + 1;
-        if (!wait(&p_full[i], s & 1, a.status, abort_flag) || !full(seq)) return false;
+        const uint32_t seq = seq0 + seq_of(i, s) + 1, st = seq % C::kStages;
+        if (!wait(&p_full[i], ((i ? done1 : done0) + s) & 1, a.status, abort_flag) || !full(seq)) return false;
         tc_fence_after();
-        const uint32_t v0 = smem_u32(sStage + (seq % C::kStages) * C::kStage);
+        if (elect_one()) {
+          const uint64_t v0 = dV + st * (C::kStage / 16);
 #pragma unroll
-        for (int ks = 0; ks < BN / 16; ++ks)
-          umma_f16_ts(tmem + kColO + D * i, tmem + kColS + 128 * i + ks * 8,
-                      make_sdesc(v0 + ks * 2048, BN * 128, 1024, kLayoutSW128), idesc_pv, (s | ks) ? 1u : 0u);
-        if (!SHARED || i == 1 || s >= n1) umma_commit(&kv_empty[seq % C::kStages]);
-        if (s + 1 == (i ? n1 : n0)) umma_commit(&o_full[i]);
+          for (int ks = 0; ks < BN / 16; ++ks)
+            umma_f16_ts(tmem + kColO + D * i, tmem + kColS + 128 * i + ks * 8, v0 + ks * 128, idesc_pv, (s | ks) ? 1u : 0u);
+          if (!SHARED || i == 1 || s >= n1) umma_commit(&kv_empty[st]);
+          if (s + 1 == (i ? n1 : n0)) umma_commit(&o_full[i]);
+        }
+        __syncwarp();
         return true;
       };
-      bool ok = wait(q_full, 0, a.status, abort_flag);
+      ok = wait(q_full, seg & 1, a.status, abort_flag);
       if (ok && n0 > 0) ok = qk(0, 0);
       const int n = max(n0, n1);
       for (int s = 0; ok && s < n; ++s) {
@@ -225,14 +253,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && s + 1 < n0) ok = qk(0, s + 1);
         if (ok && s < n1) ok = pv(1, s);
       }
+      seq0 += 2 * n_blk_of(p);
+      done0 += n0;
+      done1 += n1;
     }
-    __syncwarp();
   } else {
     // ----------------------------------------------------------- softmax --
     const int half = warp >> 2;
     const int rt = tid & 127;                   // row of the tile
-    const int r = row0 + (SHARED ? 128 * half : 0) + rt;
-    const int n_steps = half ? n1 : n0;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + kColS + 128 * half + lane_base, tO = tmem + kColO + D * half + lane_base;
+    const float c = a.scale_log2;
+    uint32_t seq0 = 0, done = 0, outs = 0;      // ring places, steps and pieces with steps of this half so far
+    uint32_t mg = 0;                            // merge buffer uses so far
+    // the warp's place in the list is kept in shared memory between pieces
+    Work* my_work = work_s + 1 + warp;
+    if (lane == 0) *my_work = *work_s;
+    __syncwarp();
+    while (ok && my_work->n > 0) {
+    int b, g, rows, len, rbase, n_steps, n_places, blk0, bound;
+    {
+      const Work k = *my_work;
+      const Piece p = piece_of(k);
+      b = p.b;
+      g = p.g;
+      rows = p.rows;
+      len = p.len;
+      rbase = p.row0 + (SHARED ? 128 * half : 0);
+      n_steps = half ? p.n1 : p.n0;
+      n_places = 2 * n_blk_of(p);
+      blk0 = k.blk0;
+      bound = rbase + rt < rows ? max(0, min(len, p.first_pos + (rbase + rt) / a.G + 1)) : 0;   // keys this row sees
+    }
+    const int r = rbase + rt;
     {
       // q rows into the swizzled tiles (16-byte units, 8 to a 128-byte row)
       const int qt = SHARED ? half : 0;
@@ -243,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
         for (int i = lane; i < 32 * U; i += 32) {
           const int rr = wq * 32 + i / U, u = i % U;
-          const int gr = row0 + (SHARED ? 128 * half : 0) + rr;
+          const int gr = rbase + rr;
           uint4 v = make_uint4(0u, 0u, 0u, 0u);
           if (gr < rows) {
             const int t = gr / a.G, h = g * a.G + gr - t * a.G;
@@ -255,26 +308,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mbar_arrive(q_full);
     }
-    const int t_row = r / a.G;
-    const int bound = r < rows ? max(0, min(L.len, first_pos + t_row + 1)) : 0;   // keys this row sees
-    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + kColS + 128 * half + lane_base, tO = tmem + kColO + D * half + lane_base;
-    const float c = a.scale_log2;
+    const bool idle = rbase + (warp & 3) * 32 >= rows;   // no row of this warp exists: its P and O are never used
+    // nothing past the sequence's end may reach the product: the V rows there are cleared
+    auto clear_tail = [&](uint32_t seq_v, int key0) {
+      if (key0 + BN <= len) return;
+      uint8_t* vt = sStage + (seq_v % C::kStages) * C::kStage;
+      const int z0 = max(0, len - key0);
+#pragma unroll 1
+      for (int i = rt; i < (BN - z0) * C::kChunks * 8; i += 128) {
+        const int row = z0 + i / (C::kChunks * 8), u = i % (C::kChunks * 8);
+        *reinterpret_cast<uint4*>(vt + (u >> 3) * (BN * 128) + row * 128 + (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+    };
     float m_run = -INFINITY, l_run = 0.f;       // log2 domain
-    bool ok = true;
+    if (idle) {
+      for (int s = 0; ok && s < n_steps; ++s) {
+        const uint32_t seq_v = seq0 + seq_of(half, s) + 1;
+        ok = __all_sync(0xffffffffu, wait(&s_full[half], (done + s) & 1, a.status, abort_flag) &&
+                                         wait(&kv_full[seq_v % C::kStages], (seq_v / C::kStages) & 1, a.status, abort_flag));
+        if (!ok) break;
+        clear_tail(seq_v, (blk0 + (SHARED ? s : 2 * s + half)) * BN);
+        mbar_arrive(&p_full[half]);
+      }
+    } else
     for (int s = 0; s < n_steps; ++s) {
-      const int seq_v = seq_of(half, s) + 1;
+      const uint32_t seq_v = seq0 + seq_of(half, s) + 1;
       const int key0 = (blk0 + (SHARED ? s : 2 * s + half)) * BN;
-      ok = __all_sync(0xffffffffu, wait(&s_full[half], s & 1, a.status, abort_flag));
+      ok = __all_sync(0xffffffffu, wait(&s_full[half], (done + s) & 1, a.status, abort_flag));
+      if (!ok) break;
+      // the V tile's barrier also publishes the block's mapped pages
+      ok = __all_sync(0xffffffffu, wait(&kv_full[seq_v % C::kStages], (seq_v / C::kStages) & 1, a.status, abort_flag));
       if (!ok) break;
       tc_fence_after();
       uint32_t sv[128];
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * q));
       tmem_ld_wait();
-      // the V tile's barrier also publishes the block's mapped pages
-      ok = __all_sync(0xffffffffu, wait(&kv_full[seq_v % C::kStages], (seq_v / C::kStages) & 1, a.status, abort_flag));
-      if (!ok) break;
       const uint32_t mapped = mask_s[seq_v % C::kStages];
       const int vis = bound - key0;             // visible columns of this block
       const bool holes = mapped != (1u << (BN >> a.page_shift)) - 1u;
@@ -323,68 +393,137 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st32(tS + 32 * q, pk);
       }
       l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-      if (key0 + BN > L.len) {                  // the sequence's last block: nothing past its end may reach the product
-        uint8_t* vt = sStage + (seq_v % C::kStages) * C::kStage;
-        const int z0 = max(0, L.len - key0);
-        for (int i = rt; i < (BN - z0) * C::kChunks * 8; i += 128) {
-          const int row = z0 + i / (C::kChunks * 8), u = i % (C::kChunks * 8);
-          *reinterpret_cast<uint4*>(vt + (u >> 3) * (BN * 128) + row * 128 + (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-      }
+      clear_tail(seq_v, key0);
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&p_full[half]);
     }
     // ---------------------------------------------------------- epilogue --
-    const bool have = n_steps > 0;
-    if (ok && have) ok = __all_sync(0xffffffffu, wait(&o_full[half], 0, a.status, abort_flag));
-    if (ok) {
-      tc_fence_after();
-      const bool mine = r < rows;
-      const long long orow = (static_cast<long long>(b) * a.T + t_row) * a.Hq + g * a.G + (r - t_row * a.G);
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-      const bool direct = a.n_part == 1;
-      const long long n_rows = static_cast<long long>(a.B) * a.T * a.Hq;
-      const long long prow = (SHARED ? split : 2 * split + half) * n_rows + orow;
-      if (have || direct) {
-#pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
+    seq0 += n_places;
+    done += n_steps;
+    if (!ok) break;
+    if (n_steps > 0) {
+      ok = __all_sync(0xffffffffu, wait(&o_full[half], outs & 1, a.status, abort_flag));
+      ++outs;
+      if (!ok) break;
+    }
+    tc_fence_after();
+    const bool mine = r < rows;
+    const Work k = *my_work;
+    float w_own = 1.f, w_other = 0.f;           // weights of the halves' outputs (SHARED = 0)
+    const float* other = merge_s + rt * C::kMergeRow;
+    if constexpr (!SHARED) {
+      // half 1's maximum and sum, then its output 32 columns at a time, go to half 0
+      if (half) {
+        if (!wait(mg_empty, (mg & 1) ^ 1, a.status, abort_flag)) ok = false;
+        float* to = merge_s + rt * C::kMergeRow;
+        to[0] = m_run;
+        to[1] = l_run;
+        mbar_arrive(mg_full);
+        ++mg;
+        for (int c0 = 0; c0 < D; c0 += 32, ++mg) {
           uint32_t ov[32];
-          if (have) {
+          if (!idle) {
             tmem_ld32(tO + c0, ov);
             tmem_ld_wait();
           }
-          if (!mine) continue;
-          // a row without keys is 0, whatever its accumulator holds
+          ok = __all_sync(0xffffffffu, ok && wait(mg_empty, (mg & 1) ^ 1, a.status, abort_flag));
+          if (!ok) break;
+          if (mine) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            ov[i] = have && l_run > 0.f ? __float_as_uint(__uint_as_float(ov[i]) * inv) : 0u;
-          if (direct) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c0);
+            for (int i = 0; i < 8; ++i)
+              reinterpret_cast<uint4*>(to)[i] = l_run > 0.f ? make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3])
+                                                            : make_uint4(0u, 0u, 0u, 0u);
+          }
+          mbar_arrive(mg_full);
+        }
+        if (!ok) break;
+        Work next = k;
+        next_work<kTile, BN>(a, next);
+        if (lane == 0) *my_work = next;
+        __syncwarp();
+        continue;
+      }
+      ok = __all_sync(0xffffffffu, wait(mg_full, mg & 1, a.status, abort_flag));
+      if (!ok) break;
+      const float m1 = other[0], l1 = other[1];
+      mbar_arrive(mg_empty);
+      ++mg;
+      const float mt = fmaxf(m_run, m1);
+      if (mt != -INFINITY) {
+        w_own = ex2(m_run - mt);
+        w_other = ex2(m1 - mt);
+      }
+      l_run = l_run * w_own + l1 * w_other;
+      m_run = mt;
+    }
+    const int t_row = r / a.G;
+    const long long orow = (static_cast<long long>(b) * a.T + t_row) * a.Hq + g * a.G + (r - t_row * a.G);
+    const bool whole = k.n == k.all;
+    const int slot = 2 * worker + (k.blk0 == 0);
+    const int prow = slot * kTile + (SHARED ? 128 * half : 0) + rt;
+    const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 32) {
+      uint32_t ov[32];
+      if (!idle) {
+        tmem_ld32(tO + c0, ov);
+        tmem_ld_wait();
+      }
+      // a row without keys is 0, whatever its accumulator holds
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t w[4];
+      for (int i = 0; i < 32; ++i) {
+        if constexpr (!SHARED) ov[i] = w_own > 0.f ? __float_as_uint(__uint_as_float(ov[i]) * w_own) : 0u;
+        ov[i] = n_steps > 0 && l_run > 0.f ? __float_as_uint(__uint_as_float(ov[i]) * inv) : 0u;
+      }
+      if constexpr (!SHARED) {
+        ok = __all_sync(0xffffffffu, wait(mg_full, mg & 1, a.status, abort_flag));
+        if (!ok) break;
+        if (mine && l_run > 0.f) {
+          const float w = w_other * inv;
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16(__uint_as_float(ov[8 * q + 2 * e]), __uint_as_float(ov[8 * q + 2 * e + 1]));
-              dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(a.part_o + prow * D + c0);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) dst[q] = make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+          for (int i = 0; i < 8; ++i) {
+            const float4 o = reinterpret_cast<const float4*>(other)[i];
+            ov[4 * i] = __float_as_uint(fmaf(o.x, w, __uint_as_float(ov[4 * i])));
+            ov[4 * i + 1] = __float_as_uint(fmaf(o.y, w, __uint_as_float(ov[4 * i + 1])));
+            ov[4 * i + 2] = __float_as_uint(fmaf(o.z, w, __uint_as_float(ov[4 * i + 2])));
+            ov[4 * i + 3] = __float_as_uint(fmaf(o.w, w, __uint_as_float(ov[4 * i + 3])));
           }
         }
+        mbar_arrive(mg_empty);
+        ++mg;
       }
-      if (mine) {
-        if (direct) {
-          if (a.lse) a.lse[orow] = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
-        } else {
-          a.part_m[prow] = m_run;
-          a.part_l[prow] = l_run;
+      if (!mine) continue;
+      if (whole) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out + orow * D + c0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = pack_bf16(__uint_as_float(ov[8 * q + 2 * e]), __uint_as_float(ov[8 * q + 2 * e + 1]));
+          dst[q] = make_uint4(w[0], w[1], w[2], w[3]);
         }
+      } else {
+        uint4* dst = reinterpret_cast<uint4*>(a.part_o + static_cast<long long>(prow) * D + c0);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) dst[q] = make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
       }
+    }
+    if (!ok) break;
+    if (mine) {
+      if (whole) {
+        if (a.lse) a.lse[orow] = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
+      } else {
+        a.part_m[prow] = m_run;
+        a.part_l[prow] = l_run;
+      }
+    }
+    if (tid == 0 && k.blk0 == 0) a.span[static_cast<long long>(k.g) * a.B * a.tiles + k.bt] = make_longlong2(k.begin, k.all);
+    Work next = k;
+    next_work<kTile, BN>(a, next);
+    if (lane == 0) *my_work = next;
+    __syncwarp();
     }
   }
 
@@ -406,12 +545,12 @@ cudaError_t launch_t(const PagedMaps& m, const PagedArgs& a, cudaStream_t stream
   const cudaError_t e = set_max_smem(fn, smem);
   if (e != cudaSuccess) return e;
   void* args[] = {const_cast<CUtensorMap*>(&m.k), const_cast<CUtensorMap*>(&m.v), const_cast<PagedArgs*>(&a)};
-  return launch_pdl(fn, dim3(a.tiles, a.Hkv, a.B * a.n_split), dim3(kThreads), smem, stream, args);
+  return launch_pdl(fn, dim3(a.workers), dim3(kThreads), smem, stream, args);
 }
 
-// Merges the partial results of a row: f_p = l_p 2^(m_p - m*), o = sum f_p o_p / sum f_p,
-// lse = m* + log2 sum f_p. DV / 128 (at least 1) warps a row; empty parts are
-// not read.
+// Merges the pieces of the rows of cut tiles: f_p = l_p 2^(m_p - m*), o = sum
+// f_p o_p / sum f_p, lse = m* + log2 sum f_p. DV / 128 (at least 1) warps a row;
+// empty pieces are not read.
 template <int DV>
 __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedArgs a) {
   pdl_wait();
@@ -422,17 +561,26 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedArgs a) {
   const long long n_rows = static_cast<long long>(a.B) * a.T * a.Hq;
   const long long row = static_cast<long long>(blockIdx.x) * (4 / kWarps) + warp / kWarps;
   if (row >= n_rows) return;
-  const int bt = static_cast<int>(row / a.Hq), b = bt / a.T;
-  if (bt - b * a.T >= lens_of(a, b).n_new) return;      // a padding row: left as it was
-  constexpr int kRegs = kMaxParts / 32;
+  const int bt = static_cast<int>(row / a.Hq), b = bt / a.T, t = bt - b * a.T;
+  if (t >= lens_of(a, b).n_new) return;                 // a padding row: left as it was
+  const int head = static_cast<int>(row - static_cast<long long>(bt) * a.Hq), g = head / a.G;
+  const int r = t * a.G + head - g * a.G;               // row of the KV head
+  const int tile = r / a.tile_rows, in_tile = r - tile * a.tile_rows;
+  const longlong2 span = a.span[(static_cast<long long>(g) * a.B + b) * a.tiles + tile];
+  const long long total = a.head[0], used = a.head[1];
+  const int w0 = worker_of(span.x, total, used), n_part = worker_of(span.x + span.y - 1, total, used) - w0 + 1;
+  if (n_part == 1) return;                              // written by its worker
+  // row of piece p among the slots
+  auto at = [&](int p) -> long long { return static_cast<long long>(p == 0 ? 2 * w0 + 1 : 2 * (w0 + p)) * a.tile_rows + in_tile; };
+  constexpr int kRegs = kMaxWorkers / 32;
   float f[kRegs], M = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kRegs; ++i) {
     const int p = i * 32 + lane;
     f[i] = 0.f;
-    if (p < a.n_part) {
-      f[i] = a.part_l[p * n_rows + row];
-      if (f[i] > 0.f) M = fmaxf(M, a.part_m[p * n_rows + row]);
+    if (p < n_part) {
+      f[i] = a.part_l[at(p)];
+      if (f[i] > 0.f) M = fmaxf(M, a.part_m[at(p)]);
     }
   }
 #pragma unroll
@@ -441,7 +589,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedArgs a) {
 #pragma unroll
   for (int i = 0; i < kRegs; ++i) {
     const int p = i * 32 + lane;
-    if (f[i] > 0.f) f[i] *= exp2f(a.part_m[p * n_rows + row] - M);
+    if (f[i] > 0.f) f[i] *= exp2f(a.part_m[at(p)] - M);
     den += f[i];
   }
 #pragma unroll
@@ -451,17 +599,16 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedArgs a) {
   float acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  const float* src = a.part_o + row * DV + col;
   struct alignas(4 * kPer) Vec { float v[kPer]; };
 #pragma unroll
   for (int i = 0; i < kRegs; ++i) {
-    if (i * 32 >= a.n_part) break;
-    const int np = min(32, a.n_part - i * 32);
+    if (i * 32 >= n_part) break;
+    const int np = min(32, n_part - i * 32);
 #pragma unroll 8
     for (int p = 0; p < np; ++p) {
       const float w = __shfl_sync(0xffffffffu, f[i], p);
       if (w > 0.f) {
-        const Vec o = *reinterpret_cast<const Vec*>(src + (i * 32 + p) * n_rows * DV);
+        const Vec o = *reinterpret_cast<const Vec*>(a.part_o + at(i * 32 + p) * DV + col);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) acc[e] = fmaf(o.v[e], w, acc[e]);
       }

@@ -4,29 +4,42 @@
 //
 //   o[r, :] = sum_{s <= pos(r)} softmax_s(scale * q[r] . c[s]) c[s][0:512],   row r = t * Hq + head
 //
-// 128 rows are one tile; the heads of a token and the tokens of a chunk fill it
-// alike. The output alone (128 x 512 fp32) would fill an SM's tensor memory, so
-// a cluster of two CTAs shares a tile:
-//   - the score product is split over the columns: CTA 0 multiplies columns
-//     [0, 320), CTA 1 [320, 576), with its part of q in tensor memory;
-//   - each sends its partial scores of a 64-key block to the other as fp32
-//     (st.async into the partner's shared memory, counted on its mbarrier) and
-//     adds the partner's: both then hold the same bits (fp32 addition commutes)
-//     and run the same softmax;
-//   - each accumulates its 256 output columns, with P in tensor memory.
-// Per block and CTA that is 128 x 64 x (288 + 256) multiply-adds on average and
-// 32 KB exchanged; splitting the output alone would multiply the whole scores
-// in both (1.5 times the products), and 1.8 times the cache bytes would cross
-// from L2 to the SMs.
+// One pass over blocks of 128 keys with a running maximum and sum per row. 128
+// rows are one tile; the heads of a token and the tokens of a chunk fill it
+// alike.
 //
-// Tensor memory (512 columns): O 256, S 64, P 32, q 160.
+// The output of 128 rows (128 x 512 fp32) would fill an SM's tensor memory, so
+// two CTAs (a cluster) share a tile, 64 rows each, and run their products as
+// one MMA of the pair (cta_group::2): every SM stages half of the keys (Q K^T)
+// and half of the output columns (P V) and multiplies its own rows by both
+// halves. Rows never cross CTAs: each keeps its own maximum, sum and P, and the
+// pair exchanges nothing but barrier arrivals. (Splitting the products'
+// contraction instead has the CTAs exchange 32 KB of partial scores per 64 keys;
+// that measured 5.2 us a block, ten times the products themselves.)
 //
-// Threads: warps 0-7 softmax (two threads per row, each 32 of a block's 64
-// columns); warp 8 producer (TMA boxes of one page, or of the page's part of
-// the block); warp 9 MMA issuer. e4m3: warps 8-11 stage rows (codes -> bf16,
-// exact) in place of the producer and warp 12 issues. Masks, the zeroing of
-// what lies past seq_len and the handling of unmapped pages are those of
-// paged_attn.cu.
+// Per block and CTA: 128 x 128 x (576 + 512) / 2 multiply-adds (2176 cycles at
+// 4096 a cycle) against shared memory at 128 bytes a cycle: operands of Q K^T 36
+// x 4 KB, of P V 16 x 6 KB, staging 136 KB, P 16 KB: 392 KB, 3060 cycles. So
+// shared memory bounds a full pipeline, at 0.7 of the tensor rate.
+//
+// Tensor memory (512 columns): O 256, S 2 x 64. Shared memory: Q 72 KB, P 2 x 16
+// KB, a ring of seven 16 KB slots. A block takes nine of them: K as 64 keys x
+// 128 columns (five, the last half empty), V as 64 keys x 128 columns (four).
+// The products of block j + 1's scores are issued before block j's P V, so the
+// tensor cores work while a block's softmax runs.
+//
+// Threads: warps 0-3 softmax (two threads per row, 64 of the block's keys each:
+// the layout of the pair's accumulator); warp 4 loads (TMA boxes of one page, or
+// of the page's part of 64 keys); the last warp of CTA 0 issues the MMAs. e4m3:
+// warps 4-11 stage rows (codes -> bf16, exact) in place of the loads; a key's
+// scale multiplies its score and its P.
+//
+// The running maximum moves only when a block raises it by more than 2^8 (P in
+// bf16 keeps its relative precision, sums are fp32), so O is rescaled rarely.
+// Keys past a row's position are masked by select. Rows of V at and past
+// seq_len, whatever the page still holds there, are cleared in shared memory
+// before the product reads them (0 * NaN is NaN). Unmapped pages are read from
+// past the pool's last page, which TMA fills with zeros, and masked.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -37,24 +50,25 @@ namespace {
 
 using namespace paged;
 
-constexpr int BN = kPagedBNMla;
-constexpr int kStages = 3;
-constexpr int kChunks = 5;                       // 64-column chunks per CTA and block
-constexpr int kChunkBytes = BN * 128;
-constexpr int kStageBytes = kChunks * kChunkBytes;
-constexpr int kSoft = 256;
-constexpr int kXBytes = 128 * BN * 4;            // partial scores of a block: rows of 256 B, 16-byte units XOR-swizzled
+constexpr int BN = kPagedBN;
+constexpr int kRows = 128;                       // rows of a tile, 64 per CTA
+constexpr int kChunk = 64 * 128;                 // 64 keys (or rows) x 64 columns, bytes
+constexpr int kSlot = 2 * kChunk;
+constexpr int kSlots = 7;
+constexpr int kPBytes = 2 * kChunk;              // 64 rows x 128 keys
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 0, kColS = 256, kColP = 320, kColQ = 352;
-constexpr int kOffX = kStages * kStageBytes;     // [2] receive buffers
-constexpr int kOffTag = kOffX + 2 * kXBytes;     // [2][2][128] u64 tagged maxima + [2][128] u64 tagged sums
-constexpr int kOffMask = kOffTag + (4 * 128 + 2 * 128) * 8;
-constexpr int kOffKScale = (kOffMask + kStages * 8 + 15) / 16 * 16;   // read 16 bytes at a time
-constexpr int kOffBars = kOffKScale + kStages * BN * 4;
-constexpr int kNumBars = 2 * kStages + 9;
-constexpr int kOffMisc = kOffBars + kNumBars * 8;
+constexpr uint32_t kColO = 0, kColS = 256;
+constexpr int kOffP = 9 * kChunk;
+constexpr int kOffRing = kOffP + 2 * kPBytes;
+constexpr int kOffTag = kOffRing + kSlots * kSlot;   // [2][128] u64 tagged maxima, [128] u64 tagged sums
+constexpr int kOffScale = kOffTag + 3 * 128 * 8;     // e4m3: [4 warps][64] scales of the block's keys
+constexpr int kOffBars = kOffScale + 4 * 64 * 4;
+constexpr int kNumBars = 2 * kSlots + 8;
+constexpr int kOffWork = kOffBars + kNumBars * 8;
+constexpr int kOffMisc = kOffWork + sizeof(Work);
 constexpr size_t kSmem = 1024 + kOffMisc + 16;
-static_assert(kOffKScale % 16 == 0 && kOffBars % 8 == 0 && kSmem <= 227 * 1024, "shared memory layout");
+static_assert(kOffRing % 1024 == 0 && kOffScale % 16 == 0 && kOffBars % 8 == 0 && kOffWork % 8 == 0 && kSmem <= 227 * 1024,
+              "shared memory layout");
 
 __device__ __forceinline__ void put_tagged(volatile unsigned long long* slot, uint32_t tag, float v) {
   *slot = (static_cast<unsigned long long>(tag) << 32) | __float_as_uint(v);
@@ -63,10 +77,10 @@ __device__ __forceinline__ bool get_tagged(const volatile unsigned long long* sl
                                            int* status, volatile int* abort_flag) {
   unsigned long long x = *slot;
   if (static_cast<uint32_t>(x >> 32) != tag) {
-    const unsigned long long t0 = globaltimer_ns();
+    const long long t0 = clock64();
     while (static_cast<uint32_t>((x = *slot) >> 32) != tag) {
       if (*abort_flag) return false;
-      if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      if (clock64() - t0 > kWaitLimitCycles) {
         record_timeout(status);
         *abort_flag = 1;
         return false;
@@ -75,14 +89,6 @@ __device__ __forceinline__ bool get_tagged(const volatile unsigned long long* sl
   }
   *v = __uint_as_float(static_cast<uint32_t>(x));
   return true;
-}
-
-// 16 bytes into the partner's shared memory, counted on its mbarrier.
-__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t bar, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(
-                   addr),
-               "r"(bar), "r"(a), "r"(b), "r"(c), "r"(d)
-               : "memory");
 }
 
 // e4m3 pair -> bf16 pair, exact.
@@ -94,489 +100,574 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two_codes) {
 }
 
 template <bool KV8>
-constexpr int threads_of() { return KV8 ? 416 : 320; }
+constexpr int threads_of() { return KV8 ? 416 : 192; }
 
 template <bool KV8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1)
     paged_mla_kernel(const __grid_constant__ CUtensorMap tm_k, const PagedArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sStage = base;
-  uint8_t* sX = base + kOffX;
+  uint8_t* sQ = base;
+  uint8_t* sP = base + kOffP;
+  uint8_t* sRing = base + kOffRing;
   volatile unsigned long long* tag_max = reinterpret_cast<volatile unsigned long long*>(base + kOffTag);
-  volatile unsigned long long* tag_sum = tag_max + 4 * 128;
-  uint32_t* mask_s = reinterpret_cast<uint32_t*>(base + kOffMask);     // [kStages][2] rows that count
-  float* kscale_s = reinterpret_cast<float*>(base + kOffKScale);       // [kStages][BN]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(base + kOffBars);
-  uint64_t* kv_full = bars;
-  uint64_t* kv_empty = bars + kStages;
-  uint64_t* s_full = bars + 2 * kStages;
-  uint64_t* s_free = s_full + 1;
-  uint64_t* p_full = s_free + 1;
-  uint64_t* pv_done = p_full + 1;
-  uint64_t* q_ready = pv_done + 1;
-  uint64_t* x_full = q_ready + 1;      // [2] own expect_tx arrive + the partner's bytes
-  uint64_t* x_free = x_full + 2;       // [2] the partner has read what this CTA sent into its buffer i
+  volatile unsigned long long* tag_sum = tag_max + 2 * 128;
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + kOffBars);   // CTA 0: both halves of a slot are there
+  uint64_t* empty = full + kSlots;
+  uint64_t* s_full = empty + kSlots;   // [2]
+  uint64_t* p_full = s_full + 2;       // [2], CTA 0: P of both CTAs is stored
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* o_full = pv_done + 1;      // the piece's last product
+  uint64_t* q_full = o_full + 1;       // CTA 0
+  uint64_t* tail = q_full + 1;         // a slot that is cleared in part before it counts
+  Work* work_s = reinterpret_cast<Work*>(base + kOffWork);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  constexpr int kMmaWarp = KV8 ? 12 : 9;
+  constexpr int kMmaWarp = KV8 ? 12 : 5;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t rank = cluster_ctarank();
-  const uint32_t peer = rank ^ 1u;
-  const int tile = a.tiles - 1 - static_cast<int>(blockIdx.x >> 1);    // the longest rows first
-  const int split = blockIdx.y, b = blockIdx.z;
-  const int chunk0 = rank ? 4 : 0;        // global 64-column chunk of local chunk 0
-  const int nq = rank ? 4 : 5;            // chunks multiplied
-  const int qk_local0 = rank ? 1 : 0;     // local chunk of the first of them
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int worker = blockIdx.x >> 1;
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&kv_full[i], KV8 ? 128 : 1);
-      mbar_init(&kv_empty[i], 1);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&full[i], KV8 ? 16 : 2);
+      mbar_init(&empty[i], 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(s_free, kSoft);
-    mbar_init(p_full, kSoft);
-    mbar_init(pv_done, 1);
-    mbar_init(q_ready, kSoft);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&x_full[i], 1);
-      mbar_init(&x_free[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 8);
     }
+    mbar_init(pv_done, 1);
+    mbar_init(o_full, 1);
+    mbar_init(q_full, 8);
+    mbar_init(tail, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  for (int i = tid; i < 6 * 128; i += threads_of<KV8>()) tag_max[i] = 0ull;   // 0 is never a live tag
-  if (warp == kMmaWarp) {
-    tmem_alloc(tmem_slot, kTmemCols);
-    tmem_relinquish();
+  for (int i = tid; i < 3 * 128; i += threads_of<KV8>()) tag_max[i] = 0ull;   // 0 is never a live tag
+  if (warp == kMmaWarp) tmem_alloc_pair(tmem_slot, kTmemCols);
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 0) {
+    const Work k = plan_work<kRows, BN>(a, worker, a.workers);
+    if (lane == 0) *work_s = k;
   }
   tc_fence_before();
   __syncthreads();
-  tc_fence_after();
   cluster_sync_all();   // the partner's barriers are initialised before any remote arrive
-  pdl_wait();
-  pdl_trigger();
+  tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tO = tmem + kColO, tQ = tmem + kColQ, tS = tmem + kColS, tP = tmem + kColP;
-
-  const Lens L = lens_of(a, b);
-  const int rows = L.n_new * a.Hq;
-  const int row0 = tile * 128;
-  const int first_pos = L.len - L.n_new;
-  int keys = 0;                           // keys the tile's last row sees
-  if (row0 < rows) keys = max(0, min(L.len, first_pos + (min(rows, row0 + 128) - 1) / a.Hq + 1));
-  const int all = (keys + BN - 1) / BN;
-  const int per_split = (all + a.n_split - 1) / a.n_split;
-  const int blk0 = split * per_split;
-  const int nblk = max(0, min(all, blk0 + per_split) - blk0);
+  const uint32_t tO = tmem + kColO, tS = tmem + kColS;
+  const uint32_t full0 = mapa_shared(smem_u32(full), 0);         // CTA 0's barriers
+  bool ok = true;
 
   if (warp == kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer --
-    if (lane == 0 && nblk > 0) {
+    if (rank == 0) {
       const uint32_t idesc_qk = make_idesc(1, 1, 128, BN, 0, 0);
       const uint32_t idesc_pv = make_idesc(1, 1, 128, 256, 0, 1);
-      const uint32_t peer_xfree = mapa_shared(smem_u32(x_free), peer);
-      auto issue_pv = [&](int pb) -> bool {
-        if (!wait(p_full, pb & 1, a.status, abort_flag)) return false;
-        tc_fence_after();
-        const uint32_t vb = smem_u32(sStage + (pb % kStages) * kStageBytes);
+      const uint64_t dQ = make_sdesc(smem_u32(sQ), 16, 1024, kLayoutSW128);
+      const uint64_t dP = make_sdesc(smem_u32(sP), 16, 1024, kLayoutSW128);
+      const uint64_t dK = make_sdesc(smem_u32(sRing), 16, 1024, kLayoutSW128);
+      const uint64_t dV = make_sdesc(smem_u32(sRing), kChunk, 1024, kLayoutSW128);
+      int st = 0;                      // slot of the ring and the parity of its phase
+      uint32_t ph = 0;
+      auto advance = [&] {
+        if (++st == kSlots) {
+          st = 0;
+          ph ^= 1u;
+        }
+      };
+      uint32_t jb = 0, seg = 0;        // blocks and pieces so far
+      auto qk = [&](uint32_t j) -> bool {
+#pragma unroll 1
+        for (int s = 0; s < 5; ++s) {
+          if (!wait(&full[st], ph, a.status, abort_flag)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t q0 = dQ + s * (kSlot / 16), k0 = dK + st * (kSlot / 16);
+            const uint32_t d = tS + 64 * (j & 1);
 #pragma unroll
-        for (int ks = 0; ks < BN / 16; ++ks)
-          umma_f16_ts(tO, tP + ks * 8, make_sdesc(vb + ks * 2048, kChunkBytes, 1024, kLayoutSW128), idesc_pv,
-                      (pb | ks) ? 1u : 0u);
-        umma_commit(pv_done);
-        umma_commit(&kv_empty[pb % kStages]);
-        // P(pb) is stored, so every softmax thread has read block pb's partial
-        // scores from buffer pb & 1: the partner may send block pb + 2 into it
-        mbar_arrive_remote(peer_xfree + (pb & 1) * 8);
+            for (int i = 0; i < 4; ++i) umma_f16_pair(d, q0 + 2 * i, k0 + 2 * i, idesc_qk, (s | i) ? 1u : 0u);
+            if (s < 4) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                umma_f16_pair(d, q0 + kChunk / 16 + 2 * i, k0 + kChunk / 16 + 2 * i, idesc_qk, 1u);
+            }
+            umma_commit_pair(&empty[st]);
+            if (s == 4) umma_commit_pair(&s_full[j & 1]);
+          }
+          __syncwarp();
+          advance();
+        }
         return true;
       };
-      bool ok = wait(q_ready, 0, a.status, abort_flag);
-      for (int blk = 0; ok && blk < nblk; ++blk) {
-        const int s = blk % kStages;
-        ok = wait(&kv_full[s], (blk / kStages) & 1, a.status, abort_flag);
-        if (ok && blk >= 1) ok = wait(s_free, (blk - 1) & 1, a.status, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t kb = smem_u32(sStage + s * kStageBytes);
+      auto pv = [&](uint32_t j, bool first, bool last) -> bool {
+        if (!wait(&p_full[j & 1], (j >> 1) & 1, a.status, abort_flag)) return false;
 #pragma unroll 1
-        for (int j = 0; j < nq; ++j) {
+        for (int i = 0; i < 4; ++i) {        // (half of the keys, half of the columns)
+          if (!wait(&full[st], ph, a.status, abort_flag)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            const int h = i >> 1, n = i & 1;
+            const uint64_t p0 = dP + ((j & 1) * kPBytes + h * kChunk) / 16, v0 = dV + st * (kSlot / 16);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_f16_ts(tS, tQ + j * 32 + ks * 8,
-                        make_sdesc(kb + (qk_local0 + j) * kChunkBytes + ks * 32, 16, 1024, kLayoutSW128), idesc_qk,
-                        (j | ks) ? 1u : 0u);
+            for (int ks = 0; ks < 4; ++ks)
+              umma_f16_pair(tO + n * 128, p0 + 2 * ks, v0 + 128 * ks, idesc_pv, first && h == 0 && ks == 0 ? 0u : 1u);
+            umma_commit_pair(&empty[st]);
+            if (i == 3) umma_commit_pair(pv_done);
+            if (i == 3 && last) umma_commit_pair(o_full);
+          }
+          __syncwarp();
+          advance();
         }
-        umma_commit(s_full);
-        if (blk >= 1) ok = issue_pv(blk - 1);
+        return true;
+      };
+      for (Work k = *work_s; ok && k.n > 0; next_work<kRows, BN>(a, k), ++seg) {
+        ok = wait(q_full, seg & 1, a.status, abort_flag) && qk(jb);
+        for (int j = 0; ok && j < k.n; ++j) {
+          if (j + 1 < k.n) ok = qk(jb + j + 1);
+          if (ok) ok = pv(jb + j, j == 0, j + 1 == k.n);
+        }
+        jb += k.n;
       }
-      if (ok) issue_pv(nblk - 1);
     }
-    __syncwarp();
-  } else if (warp >= 8) {
+  } else if (warp >= 4) {
     if constexpr (!KV8) {
       // -------------------------------------------------------- producer --
-      const int box = min(BN, 1 << a.page_shift);          // rows of a box
-      const int per = BN / box;                            // boxes of a chunk
-      const int n_ops = kChunks * per;                     // at most 20
-      const int j = lane % per, c = lane / per;
-      const int* row = a.table + static_cast<long long>(b) * a.max_pages;
-      auto page_of = [&](int blk) -> int {
-        const int tok = (blk0 + blk) * BN + j * box;
-        if (blk >= nblk || tok >= L.len) return -1;
-        const int p = __ldg(row + (tok >> a.page_shift));
-        if (p < 0 || p >= a.n_pages) {
-          if (c == 0 && rank == 0) record_bad_page(a.status);
-          return -1;
-        }
-        return p;
-      };
-      int next = page_of(0);
-      bool ok = true;
-      for (int blk = 0; ok && blk < nblk; ++blk) {
-        const int page = next;
-        next = page_of(blk + 1);
-        const int s = blk % kStages;
-        if (blk >= kStages) {
-          ok = __all_sync(0xffffffffu, wait(&kv_empty[s], ((blk / kStages) - 1) & 1, a.status, abort_flag));
-          if (!ok) break;
-        }
-        // rows of the block that count: mapped, below seq_len
-        const uint32_t mapped = __ballot_sync(0xffffffffu, page >= 0);
-        if (lane < 2) {
-          uint32_t m = 0u;
-          const int left = L.len - (blk0 + blk) * BN - 32 * lane;       // rows of this word below seq_len
-          for (int i = 0; i < 32; i += 16)
-            if ((mapped >> ((32 * lane + i) / box)) & 1u) m |= 0xFFFFu << i;
-          if (left < 32) m &= left > 0 ? (1u << left) - 1u : 0u;
-          mask_s[2 * s + lane] = m;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&kv_full[s], kStageBytes);
-        __syncwarp();
-        if (lane < n_ops) {
-          const int tok = (blk0 + blk) * BN + j * box;
-          tma_load_page(sStage + s * kStageBytes + c * kChunkBytes + j * box * 128, &tm_k, &kv_full[s], (chunk0 + c) * 64,
-                        tok & ((1 << a.page_shift) - 1), page >= 0 ? page : a.n_pages);
+      const int box = min(kPagedBox, 1 << a.page_shift);         // rows of a box
+      const int per = 64 / box;                                  // boxes of 64 keys
+      const int c = lane / per, i = lane - c * per;              // this lane's box: chunk c, rows i * box
+      int st = 0;
+      uint32_t ph = 1, n_tail = 0;                               // the ring starts empty
+      for (Work k = *work_s; ok && k.n > 0; next_work<kRows, BN>(a, k)) {
+        const int b = k.bt / a.tiles;
+        const Lens L = lens_of(a, b);
+        const int* row = a.table + static_cast<long long>(b) * a.max_pages;
+        // lane g < 8: the page of the block's keys [16 g, 16 g + 16), -1: nothing there
+        auto pages_of = [&](int j) -> int {
+          const int tok = (k.blk0 + j) * BN + lane * 16;
+          if (lane >= 8 || j >= k.n || tok >= L.len) return -1;
+          const int p = __ldg(row + (tok >> a.page_shift));
+          if (p < 0 || p >= a.n_pages) {
+            record_bad_page(a.status);
+            return -1;
+          }
+          return p;
+        };
+        // a slot: 64 keys from `key` of block j, `nc` chunks of columns from `chunk`
+        auto load = [&](int j, int pages, int key, int chunk, int nc, bool is_v) -> bool {
+          if (!__all_sync(0xffffffffu, wait(&empty[st], ph, a.status, abort_flag))) return false;
+          const int tok = (k.blk0 + j) * BN + key;
+          const int page = __shfl_sync(0xffffffffu, pages, ((key + i * box) >> 4) & 31);
+          const int rows = L.len - tok;                          // rows that hold a token
+          const bool clear = is_v && rows > 0 && rows < 64;
+          if (lane == 0) {
+            if (clear) mbar_arrive_expect_tx(tail, nc * kChunk);
+            else mbar_arrive_expect_tx_at(full0 + st * 8, nc * kChunk);
+          }
+          __syncwarp();
+          uint8_t* dst = sRing + st * kSlot;
+          if (lane < nc * per) {
+            const int in_page = (tok + i * box) & ((1 << a.page_shift) - 1);
+            if (clear)
+              tma_load_page(dst + c * kChunk + i * box * 128, &tm_k, tail, (chunk + c) * 64, in_page, page >= 0 ? page : a.n_pages);
+            else
+              tma_load_page_pair(dst + c * kChunk + i * box * 128, &tm_k, full0 + st * 8, (chunk + c) * 64, in_page,
+                                 page >= 0 ? page : a.n_pages);
+          }
+          if (clear) {
+            if (!__all_sync(0xffffffffu, wait(tail, n_tail & 1, a.status, abort_flag))) return false;
+            ++n_tail;
+            for (int z = lane; z < (64 - rows) * 16; z += 32) {
+              const int zr = rows + (z >> 4), u = z & 15;
+              *reinterpret_cast<uint4*>(dst + (u >> 3) * kChunk + zr * 128 + (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_at(full0 + st * 8);
+          }
+          if (++st == kSlots) {
+            st = 0;
+            ph ^= 1u;
+          }
+          return true;
+        };
+        auto load_k = [&](int j, int pages) -> bool {
+          for (int s = 0; s < 5; ++s)
+            if (!load(j, pages, rank * 64, 2 * s, s < 4 ? 2 : 1, false)) return false;
+          return true;
+        };
+        auto load_v = [&](int j, int pages) -> bool {
+          for (int s = 0; s < 4; ++s)
+            if (!load(j, pages, (s >> 1) * 64, (s & 1) * 4 + rank * 2, 2, true)) return false;
+          return true;
+        };
+        int cur = pages_of(0), nxt = pages_of(1);
+        ok = load_k(0, cur);
+        for (int j = 0; ok && j < k.n; ++j) {
+          const int after = pages_of(j + 2);
+          if (j + 1 < k.n) ok = load_k(j + 1, nxt);
+          if (ok) ok = load_v(j, cur);
+          cur = nxt;
+          nxt = after;
         }
       }
     } else {
       // --------------------------------------------- e4m3: stage the rows --
-      // Thread: half (160 codes) of a row's 320 columns. Its next block's codes
-      // are loaded before this one's are converted.
-      const int ct = tid - 256;
-      const int row = ct & 63, part = ct >> 6;
-      const int* trow = a.table + static_cast<long long>(b) * a.max_pages;
-      constexpr int kU = kChunks * 4 / 2;                  // 16-code units of the thread
-      uint4 v[kU];
-      float sc;
-      bool live;
-      auto load = [&](int blk) {
-        const int tok = (blk0 + blk) * BN + row;
-        live = false;
-        sc = 0.f;
-        if (blk < nblk && tok < L.len) {
+      // Four threads per key, each a quarter of a slot's columns. K's codes of
+      // a block are loaded while V's of the last one are converted, and the
+      // other way round.
+      const int t = tid - 128;
+      const int row = t & 63, part = t >> 6;
+      int st = 0;
+      uint32_t ph = 1;
+      for (Work k = *work_s; ok && k.n > 0; next_work<kRows, BN>(a, k)) {
+        const int b = k.bt / a.tiles;
+        const Lens L = lens_of(a, b);
+        const int* trow = a.table + static_cast<long long>(b) * a.max_pages;
+        auto page_of = [&](int j, int h) -> int {
+          const int tok = (k.blk0 + j) * BN + h * 64 + row;
+          if (j >= k.n || tok >= L.len) return -1;
           const int p = __ldg(trow + (tok >> a.page_shift));
           if (p < 0 || p >= a.n_pages) {
-            if (rank == 0 && part == 0) record_bad_page(a.status);
-          } else {
-            live = true;
-            const int slot = tok & ((1 << a.page_shift) - 1);
-            const uint4* src = reinterpret_cast<const uint4*>(a.kv8 + p * a.kv8_page + slot * a.kv8_row + chunk0 * 64) +
-                               part * kU;
-            sc = __ldg(a.k_scale + (static_cast<long long>(p) << a.page_shift) + slot);
-#pragma unroll
-            for (int i = 0; i < kU; ++i) v[i] = __ldg(src + i);
+            if (part == 0) record_bad_page(a.status);
+            return -1;
           }
-        }
-        if (!live) {
+          return p;
+        };
+        auto row_of = [&](int j, int h, int page) -> const uint4* {
+          const int tok = (k.blk0 + j) * BN + h * 64 + row;
+          return reinterpret_cast<const uint4*>(a.kv8 + page * a.kv8_page + (tok & ((1 << a.page_shift) - 1)) * a.kv8_row);
+        };
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        uint4 vk[9], vv[8];
+        auto load_k = [&](int j, int page) {
+          if (page < 0) {
 #pragma unroll
-          for (int i = 0; i < kU; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
-        }
-      };
-      load(0);
-      for (int blk = 0; blk < nblk; ++blk) {
-        const int s = blk % kStages;
-        if (blk >= kStages &&
-            !__all_sync(0xffffffffu, wait(&kv_empty[s], ((blk / kStages) - 1) & 1, a.status, abort_flag)))
-          break;
-        const uint32_t m = __ballot_sync(0xffffffffu, live);
-        if (part == 0) {
-          if (lane == 0) mask_s[2 * s + (row >> 5)] = m;
-          kscale_s[s * BN + row] = sc;
-        }
-        uint8_t* dst = sStage + s * kStageBytes + row * 128;
-        const int swz = row & 7;
+            for (int i = 0; i < 9; ++i) vk[i] = zero;
+            return;
+          }
+          const uint4* src = row_of(j, rank, page);
 #pragma unroll
-        for (int i = 0; i < kU; ++i) {
-          const int u = part * kU + i, c = u >> 2, q = u & 3;
-          const uint4 e = v[i];
-          *reinterpret_cast<uint4*>(dst + c * kChunkBytes + (((2 * q) ^ swz) << 4)) =
-              make_uint4(e4m3x2_to_bf16x2(e.x), e4m3x2_to_bf16x2(e.x >> 16), e4m3x2_to_bf16x2(e.y),
-                         e4m3x2_to_bf16x2(e.y >> 16));
-          *reinterpret_cast<uint4*>(dst + c * kChunkBytes + (((2 * q + 1) ^ swz) << 4)) =
-              make_uint4(e4m3x2_to_bf16x2(e.z), e4m3x2_to_bf16x2(e.z >> 16), e4m3x2_to_bf16x2(e.w),
-                         e4m3x2_to_bf16x2(e.w >> 16));
+          for (int s = 0; s < 4; ++s) {
+            vk[2 * s] = __ldg(src + s * 8 + part * 2);
+            vk[2 * s + 1] = __ldg(src + s * 8 + part * 2 + 1);
+          }
+          vk[8] = __ldg(src + 32 + part);
+        };
+        auto load_v = [&](int j, int page0, int page1) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int page = h ? page1 : page0;
+            const uint4* src = page >= 0 ? row_of(j, h, page) + rank * 8 + part * 2 : nullptr;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              vv[4 * h + 2 * n] = src ? __ldg(src + n * 16) : zero;
+              vv[4 * h + 2 * n + 1] = src ? __ldg(src + n * 16 + 1) : zero;
+            }
+          }
+        };
+        auto put = [&](uint8_t* chunk, int unit, const uint4& e) {   // 16 codes -> two 16-byte units of a chunk's row
+          uint8_t* dst = chunk + row * 128;
+          *reinterpret_cast<uint4*>(dst + ((unit ^ (row & 7)) << 4)) =
+              make_uint4(e4m3x2_to_bf16x2(e.x), e4m3x2_to_bf16x2(e.x >> 16), e4m3x2_to_bf16x2(e.y), e4m3x2_to_bf16x2(e.y >> 16));
+          *reinterpret_cast<uint4*>(dst + (((unit + 1) ^ (row & 7)) << 4)) =
+              make_uint4(e4m3x2_to_bf16x2(e.z), e4m3x2_to_bf16x2(e.z >> 16), e4m3x2_to_bf16x2(e.w), e4m3x2_to_bf16x2(e.w >> 16));
+        };
+        auto emit = [&](const uint4& e0, const uint4& e1, bool two) -> bool {
+          if (!__all_sync(0xffffffffu, wait(&empty[st], ph, a.status, abort_flag))) return false;
+          uint8_t* dst = sRing + st * kSlot;
+          if (two) {
+            put(dst + (part >> 1) * kChunk, (part & 1) * 4, e0);
+            put(dst + (part >> 1) * kChunk, (part & 1) * 4 + 2, e1);
+          } else {
+            put(dst, part * 2, e0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(full0 + st * 8);
+          if (++st == kSlots) {
+            st = 0;
+            ph ^= 1u;
+          }
+          return true;
+        };
+        auto emit_k = [&]() -> bool {
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            if (!emit(vk[2 * s], vk[2 * s + 1], true)) return false;
+          return emit(vk[8], vk[8], false);
+        };
+        auto emit_v = [&]() -> bool {
+#pragma unroll
+          for (int s = 0; s < 4; ++s)
+            if (!emit(vv[2 * s], vv[2 * s + 1], true)) return false;
+          return true;
+        };
+        // pages of blocks j + 1 and j + 2 (both halves of the keys)
+        int a0 = page_of(0, 0), a1 = page_of(0, 1);
+        int n0 = page_of(1, 0), n1 = page_of(1, 1);
+        load_k(0, rank ? a1 : a0);
+        load_v(0, a0, a1);
+        ok = emit_k();
+        load_k(1, rank ? n1 : n0);
+        for (int j = 0; ok && j < k.n; ++j) {
+          const int m0 = page_of(j + 2, 0), m1 = page_of(j + 2, 1);
+          if (j + 1 < k.n) {
+            ok = emit_k();
+            if (!ok) break;
+          }
+          load_k(j + 2, rank ? m1 : m0);
+          ok = emit_v();
+          load_v(j + 1, n0, n1);
+          n0 = m0;
+          n1 = m1;
         }
-        load(blk + 1);
-        fence_proxy_async_smem();
-        mbar_arrive(&kv_full[s]);
       }
     }
   } else {
     // ------------------------------------------------- softmax / epilogue --
-    const int quarter = warp & 3, half = warp >> 2;        // columns [32 half, 32 half + 32) of a block
-    const int h = quarter * 32 + lane;                     // row of the tile
-    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const int r = row0 + h;
-    const int t_row = r / a.Hq;
-    const int bound = r < rows ? max(0, min(L.len, first_pos + t_row + 1)) : 0;
-    const long long orow = static_cast<long long>(b) * a.T * a.Hq + r;
-    bool ok = true;
-    if (nblk > 0) {
-      // q row -> TMEM columns (two bf16 per column, k ascending); the two
-      // threads of a row take alternate chunks
-      const uint4* qrow = reinterpret_cast<const uint4*>(a.q + orow * 576) + (chunk0 + qk_local0) * 8;
-#pragma unroll
-      for (int jj = 0; jj < 3; ++jj) {
-        const int j = 2 * jj + half;
-        if (j < nq) {
-          uint32_t v[32];
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const uint4 w = r < rows ? __ldg(qrow + j * 8 + t) : make_uint4(0u, 0u, 0u, 0u);
-            v[4 * t] = w.x;
-            v[4 * t + 1] = w.y;
-            v[4 * t + 2] = w.z;
-            v[4 * t + 3] = w.w;
-          }
-          tmem_st32(tQ + lane_base + j * 32, v);
-        }
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(q_ready);
-    }
-    const int swz = h & 7;   // unit t of this thread's half-row sits at unit t ^ swz
-    const uint32_t peer_x = mapa_shared(smem_u32(sX), peer) + h * (BN * 4) + half * 128;
-    const uint32_t peer_xfull = mapa_shared(smem_u32(x_full), peer);
-    const bool leader = tid == 0;
-    // Partial scores of block bb: TMEM -> registers, S freed, sent to the partner.
-    auto fetch_send = [&](int bb, uint32_t (&sv)[32]) -> bool {
-      const int i = bb & 1;
-      if (!__all_sync(0xffffffffu, wait(s_full, bb & 1, a.status, abort_flag))) return false;
-      tc_fence_after();
-      tmem_ld32(tS + lane_base + half * 32, sv);
-      if (leader) mbar_arrive_expect_tx(&x_full[i], kXBytes);   // for what the partner sends of block bb
-      tmem_ld_wait();
-      tc_fence_before();
-      mbar_arrive(s_free);
-      // the partner's buffer i holds block bb - 2 until its readers have signalled
-      if (bb >= 2 && !__all_sync(0xffffffffu, wait<true>(&x_free[i], ((bb - 2) >> 1) & 1, a.status, abort_flag)))
-        return false;
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-        st_async_v4(peer_x + i * kXBytes + ((t ^ swz) << 4), peer_xfull + i * 8, sv[4 * t], sv[4 * t + 1], sv[4 * t + 2],
-                    sv[4 * t + 3]);
-      return true;
-    };
+    const int h = tid >> 6, r = tid & 63;          // half of the block's keys, row of the CTA
+    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t p_full0 = mapa_shared(smem_u32(p_full), 0), q_full0 = mapa_shared(smem_u32(q_full), 0);
+    float* scale_s = reinterpret_cast<float*>(base + kOffScale) + warp * 64;
     const float c = a.scale_log2;
-    float m_run = -INFINITY, l_part = 0.f;   // log2 domain; l_part: this thread's columns
-    uint32_t sv_cur[32], sv_nxt[32];
-    if (nblk > 0) ok = fetch_send(0, sv_cur);
-    for (int blk = 0; ok && blk < nblk; ++blk) {
-      const int s = blk % kStages, i = blk & 1;
-      const int key0 = (blk0 + blk) * BN;
-      // Block blk + 1's partial leaves before block blk's softmax: the
-      // partner's reply then has a whole iteration to arrive.
-      if (blk + 1 < nblk) {
-        ok = fetch_send(blk + 1, sv_nxt);
-        if (!ok) break;
-      }
-      ok = __all_sync(0xffffffffu, wait<true>(&x_full[i], (blk >> 1) & 1, a.status, abort_flag));
-      if (!ok) break;
-      float x[32];
+    uint32_t jb = 0, seg = 0;
+    for (Work k = *work_s; ok && k.n > 0; next_work<kRows, BN>(a, k), ++seg) {
+      const int b = k.bt / a.tiles, row0 = (k.bt - b * a.tiles) * kRows + rank * 64;
+      const Lens L = lens_of(a, b);
+      const int rows = L.n_new * a.Hq;
+      const int* trow = a.table + static_cast<long long>(b) * a.max_pages;
+      const long long q0 = static_cast<long long>(b) * a.T * a.Hq + row0;   // the CTA's first row of q and out
       {
-        const float4* src = reinterpret_cast<const float4*>(sX + i * kXBytes + h * (BN * 4) + half * 128);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const float4 w = src[t ^ swz];
-          x[4 * t] = __uint_as_float(sv_cur[4 * t]) + w.x;
-          x[4 * t + 1] = __uint_as_float(sv_cur[4 * t + 1]) + w.y;
-          x[4 * t + 2] = __uint_as_float(sv_cur[4 * t + 2]) + w.z;
-          x[4 * t + 3] = __uint_as_float(sv_cur[4 * t + 3]) + w.w;
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + q0 * 576);
+        const int live = (rows - row0) * 72;       // 16-byte units that exist
+#pragma unroll 9
+        for (int i = tid; i < 64 * 72; i += 128) {
+          const int rr = i / 72, u = i - rr * 72;
+          const uint4 v = i < live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(sQ + (u >> 3) * kChunk + rr * 128 + (((u & 7) ^ (rr & 7)) << 4)) = v;
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(q_full0);
       }
-      ok = __all_sync(0xffffffffu, wait(&kv_full[s], (blk / kStages) & 1, a.status, abort_flag));
-      if (!ok) break;
-      const float4* ks4 = reinterpret_cast<const float4*>(kscale_s + s * BN + 32 * half);   // KV8: token scales
+      const int bound = row0 + r < rows ? max(0, min(L.len, L.len - L.n_new + (row0 + r) / a.Hq + 1)) : 0;   // keys this row sees
+      // lane g < 8: whether the block's keys [16 g, 16 g + 16) have a page
+      auto has_page = [&](int j) -> bool {
+        const int tok = (k.blk0 + j) * BN + lane * 16;
+        if (lane >= 8 || j >= k.n || tok >= L.len) return false;
+        const int p = __ldg(trow + (tok >> a.page_shift));
+        return p >= 0 && p < a.n_pages;
+      };
+      // e4m3: the scale of key 64 h + i of block j (0 where there is none)
+      auto page_at = [&](int j, int i) -> int {
+        const int tok = (k.blk0 + j) * BN + 64 * h + i;
+        if (j >= k.n || tok >= L.len) return -1;
+        const int p = __ldg(trow + (tok >> a.page_shift));
+        return p < a.n_pages ? p : -1;
+      };
+      auto scale_at = [&](int j, int i, int page) -> float {
+        const int tok = (k.blk0 + j) * BN + 64 * h + i;
+        return page < 0 ? 0.f
+                        : __ldg(a.k_scale + (static_cast<long long>(page) << a.page_shift) + (tok & ((1 << a.page_shift) - 1)));
+      };
+      bool page_next = has_page(0);
+      float sc0 = 0.f, sc1 = 0.f;
+      int pg0 = -1, pg1 = -1;
       if constexpr (KV8) {
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const float4 k4 = ks4[t];
-          x[4 * t] *= k4.x;
-          x[4 * t + 1] *= k4.y;
-          x[4 * t + 2] *= k4.z;
-          x[4 * t + 3] *= k4.w;
+        sc0 = scale_at(0, lane, page_at(0, lane));
+        sc1 = scale_at(0, lane + 32, page_at(0, lane + 32));
+        pg0 = page_at(1, lane);
+        pg1 = page_at(1, lane + 32);
+      }
+      float m_run = -INFINITY, l_part = 0.f;       // log2 domain; l_part: this thread's keys
+      for (int j = 0; j < k.n; ++j) {
+        const uint32_t at = jb + j;
+        const int key0 = (k.blk0 + j) * BN + 64 * h;
+        const uint32_t pages = __ballot_sync(0xffffffffu, page_next) >> (4 * h) & 0xFu;
+        page_next = has_page(j + 1);
+        if constexpr (KV8) {
+          __syncwarp();
+          scale_s[lane] = sc0;
+          scale_s[lane + 32] = sc1;
+          __syncwarp();
+          sc0 = scale_at(j + 1, lane, pg0);
+          sc1 = scale_at(j + 1, lane + 32, pg1);
+          pg0 = page_at(j + 2, lane);
+          pg1 = page_at(j + 2, lane + 32);
         }
-      }
-      const uint32_t counts = mask_s[2 * s + half];
-      const int vis = bound - key0 - 32 * half;
-      if (__any_sync(0xffffffffu, vis < 32) || counts != 0xFFFFFFFFu) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j >= vis || !((counts >> j) & 1u)) x[j] = -INFINITY;
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
-      const float mb_mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-      put_tagged(tag_max + (i * 2 + half) * 128 + h, static_cast<uint32_t>(blk + 1), mb_mine);
-      float mb_other;
-      ok = __all_sync(0xffffffffu, get_tagged(tag_max + (i * 2 + (half ^ 1)) * 128 + h, static_cast<uint32_t>(blk + 1),
-                                              &mb_other, a.status, abort_flag));
-      if (!ok) break;
-      const float mb = fmaxf(mb_mine, mb_other);
-      const bool move = mb > m_run + 8.f || (m_run == -INFINITY && mb != -INFINITY);
-      float corr = 1.f;
-      if (move) {
-        corr = m_run == -INFINITY ? 0.f : ex2(m_run - mb);
-        l_part *= corr;
-        m_run = mb;
-      }
-      const float mu = m_run == -INFINITY ? 0.f : m_run;
-      float ps[4] = {0.f, 0.f, 0.f, 0.f};
-      uint32_t pk[16];
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        float p0 = ex2(fmaf(x[j], c, -mu)), p1 = ex2(fmaf(x[j + 1], c, -mu));
-        ps[(j >> 1) & 3] += p0 + p1;
-        if constexpr (KV8) {   // V row = code * scale: the scale rides on P
-          const float2 k2 = reinterpret_cast<const float2*>(ks4)[j >> 1];
-          p0 *= k2.x;
-          p1 *= k2.y;
-        }
-        pk[j >> 1] = pack_bf16(p0, p1);
-      }
-      l_part += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-      // P and O are free once PV(blk - 1) has completed
-      if (blk >= 1) {
-        ok = __all_sync(0xffffffffu, wait(pv_done, (blk - 1) & 1, a.status, abort_flag));
+        ok = __all_sync(0xffffffffu, wait(&s_full[at & 1], (at >> 1) & 1, a.status, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        if (__any_sync(0xffffffffu, move)) {   // rescale this thread's 128 of the 256 columns
+        float x[64];
+        {
+          uint32_t s0[32], s1[32];
+          tmem_ld32(tS + lane_base + 64 * (at & 1), s0);
+          tmem_ld32(tS + lane_base + 64 * (at & 1) + 32, s1);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            x[i] = __uint_as_float(s0[i]);
+            x[32 + i] = __uint_as_float(s1[i]);
+          }
+        }
+        const float4* ks4 = reinterpret_cast<const float4*>(scale_s);
+        if constexpr (KV8) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float4 k4 = ks4[i];
+            x[4 * i] *= k4.x;
+            x[4 * i + 1] *= k4.y;
+            x[4 * i + 2] *= k4.z;
+            x[4 * i + 3] *= k4.w;
+          }
+        }
+        const int vis = bound - key0;              // visible keys of this half block
+        if (__any_sync(0xffffffffu, vis < 64) || pages != 0xFu) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i >= vis || !((pages >> (i >> 4)) & 1u)) x[i] = -INFINITY;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
+        const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+        // the row's other half: the partner is at the same block, one block's slots are read before they are written again
+        put_tagged(tag_max + (at & 1) * 128 + tid, at + 1, mine);
+        float other;
+        ok = __all_sync(0xffffffffu, get_tagged(tag_max + (at & 1) * 128 + (tid ^ 64), at + 1, &other, a.status, abort_flag));
+        if (!ok) break;
+        const float mb = fmaxf(mine, other);
+        const bool move = mb > m_run + 8.f || (m_run == -INFINITY && mb != -INFINITY);
+        float corr = 1.f;
+        if (move) {
+          corr = m_run == -INFINITY ? 0.f : ex2(m_run - mb);
+          l_part *= corr;
+          m_run = mb;
+        }
+        const float mu = m_run == -INFINITY ? 0.f : m_run;   // all masked so far: exp2(-inf) = 0
+        // P of block at - 2 has been read: its product was issued before the scores of this block
+        uint8_t* prow = sP + (at & 1) * kPBytes + h * kChunk + r * 128;
+        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = 8 * u + 2 * e;
+            float p0 = ex2(fmaf(x[i], c, -mu)), p1 = ex2(fmaf(x[i + 1], c, -mu));
+            ps[e] += p0 + p1;
+            if constexpr (KV8) {                   // V row = code * scale: the scale rides on P
+              const float2 k2 = reinterpret_cast<const float2*>(scale_s)[i >> 1];
+              p0 *= k2.x;
+              p1 *= k2.y;
+            }
+            w[e] = pack_bf16(p0, p1);
+          }
+          *reinterpret_cast<uint4*>(prow + ((u ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        l_part += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        if (j > 0 && __any_sync(0xffffffffu, move)) {   // rescale this thread's part of O
+          // (at most this block's product is unfinished besides: the scores at hand were issued after all before it)
+          ok = __all_sync(0xffffffffu, wait(pv_done, (at - 1) & 1, a.status, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll 1
-          for (int c0 = half * 128; c0 < half * 128 + 128; c0 += 32) {
+          for (int c0 = 0; c0 < 256; c0 += 32) {
             uint32_t ov[32];
             tmem_ld32(tO + lane_base + c0, ov);
             tmem_ld_wait();
 #pragma unroll
-            for (int t = 0; t < 32; ++t) ov[t] = __float_as_uint(__uint_as_float(ov[t]) * corr);
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * corr);
             tmem_st32(tO + lane_base + c0, ov);
           }
-        }
-      }
-      tmem_st16(tP + lane_base + half * 16, pk);   // keys [32 half, 32 half + 32) of the row
-      if (!KV8 && key0 + BN > L.len) {             // nothing past the sequence's end may reach the product
-        const int z0 = max(0, L.len - key0);
-        for (int z = tid; z < (BN - z0) * 32; z += kSoft) {
-          const int zr = z0 + (z >> 5), u = z & 31;
-          *reinterpret_cast<uint4*>(sStage + s * kStageBytes + (u >> 3) * kChunkBytes + zr * 128 + (u & 7) * 16) =
-              make_uint4(0u, 0u, 0u, 0u);
+          tmem_st_wait();
         }
         fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(p_full0 + (at & 1) * 8);
       }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(p_full);
-#pragma unroll
-      for (int t = 0; t < 32; ++t) sv_cur[t] = sv_nxt[t];
-    }
-    if (ok && nblk > 0) ok = __all_sync(0xffffffffu, wait(pv_done, (nblk - 1) & 1, a.status, abort_flag));
-    // row sum over both halves (fixed order: both threads get the same value)
-    float l_run = 0.f;
-    if (ok) {
-      put_tagged(tag_sum + half * 128 + h, 0xFFFFFFFFu, l_part);
+      jb += k.n;
+      if (ok) ok = __all_sync(0xffffffffu, wait(o_full, seg & 1, a.status, abort_flag));
+      if (!ok) break;
+      // row sum over both halves (fixed order: both threads get the same value)
+      put_tagged(tag_sum + tid, seg + 1, l_part);
       float l_other;
-      ok = __all_sync(0xffffffffu,
-                      get_tagged(tag_sum + (half ^ 1) * 128 + h, 0xFFFFFFFFu, &l_other, a.status, abort_flag));
-      l_run = half == 0 ? l_part + l_other : l_other + l_part;
-    }
-    // ---- epilogue: this thread's 128 output columns, staged per warp for coalesced stores
-    if (ok) {
+      ok = __all_sync(0xffffffffu, get_tagged(tag_sum + (tid ^ 64), seg + 1, &l_other, a.status, abort_flag));
+      if (!ok) break;
+      const float l_run = h == 0 ? l_part + l_other : l_other + l_part;
+      // ---- epilogue: the accumulator holds columns [256 n + 128 h, + 128) of the row, n = 0, 1; staged per warp
+      // (in P's buffers) for coalesced stores
       tc_fence_after();
-      const bool have = nblk > 0;
-      const bool direct = a.n_part == 1;
-      const long long n_rows = static_cast<long long>(a.B) * a.T * a.Hq;
+      const bool whole = k.n == k.all;
+      const int slot = 2 * worker + (k.blk0 == 0);
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-      if (have || direct) {
-        float* tile_s = reinterpret_cast<float*>(sX) + warp * 32 * 36;   // [32 rows][36]
+      const int wrow = (warp & 1) * 32;            // the warp's first row
+      float* tile_s = reinterpret_cast<float*>(sP) + warp * 32 * 36;   // [32 rows][36]
 #pragma unroll 1
-        for (int c0 = half * 128; c0 < half * 128 + 128; c0 += 32) {
-          uint32_t ov[32];
-          if (have) {
-            tmem_ld32(tO + lane_base + c0, ov);
-            tmem_ld_wait();
-          }
-          float4* trow = reinterpret_cast<float4*>(tile_s + lane * 36);
+      for (int q = 0; q < 8; ++q) {
+        uint32_t ov[32];
+        tmem_ld32(tO + lane_base + q * 32, ov);
+        tmem_ld_wait();
+        float4* mine4 = reinterpret_cast<float4*>(tile_s + lane * 36);
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);   // a row without keys is 0
-            if (have && l_run > 0.f)
-              w = make_float4(__uint_as_float(ov[4 * t]) * inv, __uint_as_float(ov[4 * t + 1]) * inv,
-                              __uint_as_float(ov[4 * t + 2]) * inv, __uint_as_float(ov[4 * t + 3]) * inv);
-            trow[t] = w;
-          }
-          __syncwarp();
-          if (direct) {
-            // 8 rows per instruction, 64 bytes (32 bf16) per row
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const int rr = t * 8 + (lane >> 2), seg = lane & 3;
-              const int gr = row0 + quarter * 32 + rr;
-              const float4* sp = reinterpret_cast<const float4*>(tile_s + rr * 36 + seg * 8);
-              const float4 v0 = sp[0], v1 = sp[1];
-              if (gr < rows)
-                *reinterpret_cast<uint4*>(a.out + (static_cast<long long>(b) * a.T * a.Hq + gr) * 512 + rank * 256 + c0 +
-                                          seg * 8) =
-                    make_uint4(pack_bf16(v0.x, v0.y), pack_bf16(v0.z, v0.w), pack_bf16(v1.x, v1.y), pack_bf16(v1.z, v1.w));
-            }
-          } else {
-            // 4 rows per instruction, 128 bytes (32 fp32) per row
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
-              const int rr = t * 4 + (lane >> 3), seg = lane & 7;
-              const int gr = row0 + quarter * 32 + rr;
-              const float4 v0 = *reinterpret_cast<const float4*>(tile_s + rr * 36 + seg * 4);
-              if (gr < rows)
-                *reinterpret_cast<float4*>(
-                    a.part_o + (split * n_rows + static_cast<long long>(b) * a.T * a.Hq + gr) * 512 + rank * 256 + c0 +
-                    seg * 4) = v0;
-            }
-          }
-          __syncwarp();
+        for (int i = 0; i < 8; ++i) {
+          float4 w = make_float4(0.f, 0.f, 0.f, 0.f);      // a row without keys is 0
+          if (l_run > 0.f)
+            w = make_float4(__uint_as_float(ov[4 * i]) * inv, __uint_as_float(ov[4 * i + 1]) * inv,
+                            __uint_as_float(ov[4 * i + 2]) * inv, __uint_as_float(ov[4 * i + 3]) * inv);
+          mine4[i] = w;
         }
-      }
-      if (rank == 0 && half == 0 && r < rows) {
-        if (direct) {
-          if (a.lse) a.lse[orow] = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
+        __syncwarp();
+        const int col = (q >> 2) * 256 + h * 128 + (q & 3) * 32;
+        if (whole) {
+          // 8 rows per instruction, 64 bytes (32 bf16) per row
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = i * 8 + (lane >> 2), sg = lane & 3;
+            const float4* sp = reinterpret_cast<const float4*>(tile_s + rr * 36 + sg * 8);
+            const float4 v0 = sp[0], v1 = sp[1];
+            if (row0 + wrow + rr < rows)
+              *reinterpret_cast<uint4*>(a.out + (q0 + wrow + rr) * 512 + col + sg * 8) =
+                  make_uint4(pack_bf16(v0.x, v0.y), pack_bf16(v0.z, v0.w), pack_bf16(v1.x, v1.y), pack_bf16(v1.z, v1.w));
+          }
         } else {
-          a.part_m[split * n_rows + orow] = m_run;
-          a.part_l[split * n_rows + orow] = l_run;
+          // 4 rows per instruction, 128 bytes (32 fp32) per row
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int rr = i * 4 + (lane >> 3), sg = lane & 7;
+            const float4 v0 = *reinterpret_cast<const float4*>(tile_s + rr * 36 + sg * 4);
+            if (row0 + wrow + rr < rows)
+              *reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(slot) * kRows + rank * 64 + wrow + rr) * 512 + col +
+                                         sg * 4) = v0;
+          }
+        }
+        __syncwarp();
+      }
+      if (h == 0 && row0 + r < rows) {
+        if (whole) {
+          if (a.lse) a.lse[q0 + r] = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
+        } else {
+          a.part_m[slot * kRows + rank * 64 + r] = m_run;
+          a.part_l[slot * kRows + rank * 64 + r] = l_run;
         }
       }
+      if (tid == 0 && rank == 0 && k.blk0 == 0) a.span[k.bt] = make_longlong2(k.begin, k.all);
     }
   }
 
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) spin_ns(50000);   // let copies and MMAs in flight land before the exit
-  cluster_sync_all();                // the partner has finished writing into this CTA's shared memory
+  cluster_sync_all();                // no barrier of this CTA is used by the partner any more
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 
@@ -589,8 +680,7 @@ cudaError_t launch_paged_mla(const PagedMaps& m, const PagedArgs& a, cudaStream_
   const cudaError_t e = set_max_smem(fn, kSmem);
   if (e != cudaSuccess) return e;
   void* args[] = {const_cast<CUtensorMap*>(&m.k), const_cast<PagedArgs*>(&a)};
-  return launch_pdl(fn, dim3(2 * a.tiles, a.n_split, a.B), dim3(kv8 ? threads_of<true>() : threads_of<false>()), kSmem,
-                    stream, args);
+  return launch_pdl(fn, dim3(2 * a.workers), dim3(kv8 ? threads_of<true>() : threads_of<false>()), kSmem, stream, args);
 }
 
 }  // namespace lsa

@@ -147,7 +147,7 @@ def test_paged_attention_refusals_of_out_and_workspace():
     lib = L.load()
     pi = _paged()
     n = L.workspace_size(L.LSA_OP_PAGED_ATTN, paged=pi)
-    assert n > 0 and n % 256 == 0                          # two short batches are split over the GPU
+    assert n > 0 and n % 256 == 0
     ok = (ctypes.byref(pi), 7 * MB, None)
     assert lib.lsa_paged_attn(ctypes.byref(pi), None, None, 256, n, None) == INVALID
     assert lib.lsa_paged_attn(ctypes.byref(pi), 7 * MB + 2, None, 256, n, None) == INVALID
@@ -156,8 +156,10 @@ def test_paged_attention_refusals_of_out_and_workspace():
     assert lib.lsa_paged_attn(*ok, None, n, None) == INVALID
     assert lib.lsa_paged_attn(*ok, 128, n, None) == INVALID
     assert lib.lsa_paged_attn(None, 7 * MB, None, None, 0, None) == INVALID
-    # many rows fill the GPU by themselves: no partial results
-    assert L.workspace_size(L.LSA_OP_PAGED_ATTN, paged=_paged(B=8, T=4000, Hq=128)) == 0
+    # pieces of cut tiles: two per worker (a pair of SMs), whatever the number of rows, and a span for every tile
+    big = L.workspace_size(L.LSA_OP_PAGED_ATTN, paged=_paged(B=8, T=4000, Hq=128, max_pages=4000))
+    small = L.workspace_size(L.LSA_OP_PAGED_ATTN, paged=_paged(B=8, T=1, Hq=128, max_pages=4000))
+    assert big - small == 8 * 4000 * 16 - 256
 
 
 def test_upkeep_refusals():
