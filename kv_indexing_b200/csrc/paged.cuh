@@ -144,6 +144,8 @@ __device__ __forceinline__ int worker_of(long long x, long long total, long long
   return static_cast<int>(((x + 1) * used - 1) / total);
 }
 
+constexpr int kNoPage = -2147483647 - 1;   // past the sequence's end (other entries outside the pool are reported)
+
 // One lane of the warp (the same one every time).
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;

@@ -169,20 +169,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Piece p = piece_of(k);
       const int n_blk = n_blk_of(p);
       const int* row = a.table + static_cast<long long>(p.b) * a.max_pages;
-      auto page_of = [&](int blk) -> int {     // physical page of this lane's page of the block; -1: nothing there
+      auto page_of = [&](int blk) -> int {     // physical page of this lane's page of the block
         const int tok = (k.blk0 + blk) * BN + (j << a.page_shift);
-        if (blk >= n_blk || tok >= p.len) return -1;
-        const int pg = __ldg(row + (tok >> a.page_shift));
-        if (pg < 0 || pg >= a.n_pages) {
-          if (c == 0) record_bad_page(a.status);
-          return -1;
-        }
-        return pg;
+        return blk < n_blk && tok < p.len ? __ldg(row + (tok >> a.page_shift)) : kNoPage;
       };
       int next = page_of(0);
       for (int blk = 0; ok && blk < n_blk; ++blk) {
-        const int page = next;
-        next = page_of(blk + 1);
+        int page = next;
+        next = page_of(blk + 1);               // not looked at before the next block: the load takes its time
+        if (page < 0 || page >= a.n_pages) {
+          if (page != kNoPage && c == 0) record_bad_page(a.status);
+          page = -1;
+        }
         const uint32_t mapped = __ballot_sync(0xffffffffu, page >= 0) & ((1u << per) - 1u);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++seq) {
@@ -283,7 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       n_steps = half ? p.n1 : p.n0;
       n_places = 2 * n_blk_of(p);
       blk0 = k.blk0;
-      bound = rbase + rt < rows ? max(0, min(len, p.first_pos + (rbase + rt) / a.G + 1)) : 0;   // keys this row sees
+      // keys this row sees; rows that do not exist see all, so that they make no block a masked one
+      bound = rbase + rt < rows ? max(0, min(len, p.first_pos + (rbase + rt) / a.G + 1)) : len;
     }
     const int r = rbase + rt;
     {
@@ -341,23 +340,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, wait(&kv_full[seq_v % C::kStages], (seq_v / C::kStages) & 1, a.status, abort_flag));
       if (!ok) break;
       tc_fence_after();
-      uint32_t sv[128];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * q));
-      tmem_ld_wait();
       const uint32_t mapped = mask_s[seq_v % C::kStages];
       const int vis = bound - key0;             // visible columns of this block
-      const bool holes = mapped != (1u << (BN >> a.page_shift)) - 1u;
-      if (__any_sync(0xffffffffu, vis < BN) || holes) {
+      const bool masked = __any_sync(0xffffffffu, vis < BN) || mapped != (1u << (BN >> a.page_shift)) - 1u;
+      // The scores are read twice, for their maximum and for P: held in registers between, they would spill.
+      auto mask = [&](uint32_t (&v)[32], int q) {
 #pragma unroll
-        for (int j = 0; j < BN; ++j)
-          if (j >= vis || !((mapped >> (j >> a.page_shift)) & 1u)) sv[j] = 0xFF800000u;
-      }
+        for (int j = 0; j < 32; ++j)
+          if (32 * q + j >= vis || !((mapped >> ((32 * q + j) >> a.page_shift)) & 1u)) v[j] = 0xFF800000u;
+      };
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      {
+        uint32_t v0[32], v1[32];
 #pragma unroll
-      for (int j = 0; j < BN; j += 4)
+        for (int q = 0; q < 4; q += 2) {
+          tmem_ld32(tS + 32 * q, v0);
+          tmem_ld32(tS + 32 * q + 32, v1);
+          tmem_ld_wait();
+          if (masked) {
+            mask(v0, q);
+            mask(v1, q + 1);
+          }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], __uint_as_float(sv[j + e]));
+          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], fmaxf(__uint_as_float(v0[j]), __uint_as_float(v1[j])));
+        }
+      }
       const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
       const bool move = mb > m_run + 8.f || (m_run == -INFINITY && mb != -INFINITY);
       float corr = 1.f;
@@ -380,17 +387,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float mu = m_run == -INFINITY ? 0.f : m_run;   // all masked so far: exp2(-inf) = 0
       float ps[4] = {0.f, 0.f, 0.f, 0.f};
+      {
+        uint32_t v[2][32];
+        tmem_ld32(tS, v[0]);
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        uint32_t pk[32];
+        for (int q = 0; q < 4; ++q) {
+          tmem_ld_wait();
+          if (q < 3) tmem_ld32(tS + 32 * q + 32, v[(q + 1) & 1]);
+          uint32_t(&x)[32] = v[q & 1];
+          if (masked) mask(x, q);
+          uint32_t pk[16];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float p0 = ex2(fmaf(__uint_as_float(sv[64 * q + 2 * j]), c, -mu));
-          const float p1 = ex2(fmaf(__uint_as_float(sv[64 * q + 2 * j + 1]), c, -mu));
-          ps[j & 3] += p0 + p1;
-          pk[j] = pack_bf16(p0, p1);
+          for (int j = 0; j < 16; ++j) {
+            const float p0 = ex2(fmaf(__uint_as_float(x[2 * j]), c, -mu));
+            const float p1 = ex2(fmaf(__uint_as_float(x[2 * j + 1]), c, -mu));
+            ps[j & 3] += p0 + p1;
+            pk[j] = pack_bf16(p0, p1);
+          }
+          tmem_st16(tS + 16 * q, pk);           // over scores that have been read
         }
-        tmem_st32(tS + 32 * q, pk);
       }
       l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
       clear_tail(seq_v, key0);

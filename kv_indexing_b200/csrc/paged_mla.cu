@@ -246,16 +246,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
         const int b = k.bt / a.tiles;
         const Lens L = lens_of(a, b);
         const int* row = a.table + static_cast<long long>(b) * a.max_pages;
-        // lane g < 8: the page of the block's keys [16 g, 16 g + 16), -1: nothing there
-        auto pages_of = [&](int j) -> int {
+        // lane g < 8: the table entry of the block's keys [16 g, 16 g + 16); looked at a block later
+        auto entry_of = [&](int j) -> int {
           const int tok = (k.blk0 + j) * BN + lane * 16;
-          if (lane >= 8 || j >= k.n || tok >= L.len) return -1;
-          const int p = __ldg(row + (tok >> a.page_shift));
-          if (p < 0 || p >= a.n_pages) {
-            record_bad_page(a.status);
-            return -1;
-          }
-          return p;
+          return lane < 8 && j < k.n && tok < L.len ? __ldg(row + (tok >> a.page_shift)) : kNoPage;
+        };
+        auto page_of = [&](int p) -> int {
+          if (p >= 0 && p < a.n_pages) return p;
+          if (p != kNoPage) record_bad_page(a.status);
+          return -1;
         };
         // a slot: 64 keys from `key` of block j, `nc` chunks of columns from `chunk`
         auto load = [&](int j, int pages, int key, int chunk, int nc, bool is_v) -> bool {
@@ -305,14 +304,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
             if (!load(j, pages, (s >> 1) * 64, (s & 1) * 4 + rank * 2, 2, true)) return false;
           return true;
         };
-        int cur = pages_of(0), nxt = pages_of(1);
+        int cur = page_of(entry_of(0)), entry = entry_of(1);
         ok = load_k(0, cur);
         for (int j = 0; ok && j < k.n; ++j) {
-          const int after = pages_of(j + 2);
+          const int nxt = page_of(entry);
+          entry = entry_of(j + 2);
           if (j + 1 < k.n) ok = load_k(j + 1, nxt);
           if (ok) ok = load_v(j, cur);
           cur = nxt;
-          nxt = after;
         }
       }
     } else {
@@ -328,15 +327,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
         const int b = k.bt / a.tiles;
         const Lens L = lens_of(a, b);
         const int* trow = a.table + static_cast<long long>(b) * a.max_pages;
-        auto page_of = [&](int j, int h) -> int {
+        // the table entry of this thread's key in half h of block j; looked at a block later
+        auto entry_of = [&](int j, int h) -> int {
           const int tok = (k.blk0 + j) * BN + h * 64 + row;
-          if (j >= k.n || tok >= L.len) return -1;
-          const int p = __ldg(trow + (tok >> a.page_shift));
-          if (p < 0 || p >= a.n_pages) {
-            if (part == 0) record_bad_page(a.status);
-            return -1;
-          }
-          return p;
+          return j < k.n && tok < L.len ? __ldg(trow + (tok >> a.page_shift)) : kNoPage;
+        };
+        auto page_of = [&](int p) -> int {
+          if (p >= 0 && p < a.n_pages) return p;
+          if (p != kNoPage && part == 0) record_bad_page(a.status);
+          return -1;
         };
         auto row_of = [&](int j, int h, int page) -> const uint4* {
           const int tok = (k.blk0 + j) * BN + h * 64 + row;
@@ -407,15 +406,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
             if (!emit(vv[2 * s], vv[2 * s + 1], true)) return false;
           return true;
         };
-        // pages of blocks j + 1 and j + 2 (both halves of the keys)
-        int a0 = page_of(0, 0), a1 = page_of(0, 1);
-        int n0 = page_of(1, 0), n1 = page_of(1, 1);
-        load_k(0, rank ? a1 : a0);
-        load_v(0, a0, a1);
+        // pages of block j + 1, entries of block j + 2 (both halves of the keys)
+        int n0 = page_of(entry_of(0, 0)), n1 = page_of(entry_of(0, 1));
+        int e0 = entry_of(1, 0), e1 = entry_of(1, 1);
+        load_k(0, rank ? n1 : n0);
+        load_v(0, n0, n1);
+        n0 = page_of(e0);
+        n1 = page_of(e1);
+        e0 = entry_of(2, 0);
+        e1 = entry_of(2, 1);
         ok = emit_k();
         load_k(1, rank ? n1 : n0);
         for (int j = 0; ok && j < k.n; ++j) {
-          const int m0 = page_of(j + 2, 0), m1 = page_of(j + 2, 1);
+          const int m0 = page_of(e0), m1 = page_of(e1);
+          e0 = entry_of(j + 3, 0);
+          e1 = entry_of(j + 3, 1);
           if (j + 1 < k.n) {
             ok = emit_k();
             if (!ok) break;
@@ -455,27 +460,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
         __syncwarp();
         if (lane == 0) mbar_arrive_at(q_full0);
       }
-      const int bound = row0 + r < rows ? max(0, min(L.len, L.len - L.n_new + (row0 + r) / a.Hq + 1)) : 0;   // keys this row sees
-      // lane g < 8: whether the block's keys [16 g, 16 g + 16) have a page
-      auto has_page = [&](int j) -> bool {
+      // keys this row sees; rows that do not exist see all, so that they make no block a masked one
+      const int bound = row0 + r < rows ? max(0, min(L.len, L.len - L.n_new + (row0 + r) / a.Hq + 1)) : L.len;
+      // lane g < 8: the table entry of the block's keys [16 g, 16 g + 16), to see whether they have a page
+      auto entry_of = [&](int j) -> int {
         const int tok = (k.blk0 + j) * BN + lane * 16;
-        if (lane >= 8 || j >= k.n || tok >= L.len) return false;
-        const int p = __ldg(trow + (tok >> a.page_shift));
-        return p >= 0 && p < a.n_pages;
+        return lane < 8 && j < k.n && tok < L.len ? __ldg(trow + (tok >> a.page_shift)) : kNoPage;
       };
       // e4m3: the scale of key 64 h + i of block j (0 where there is none)
       auto page_at = [&](int j, int i) -> int {
         const int tok = (k.blk0 + j) * BN + 64 * h + i;
-        if (j >= k.n || tok >= L.len) return -1;
-        const int p = __ldg(trow + (tok >> a.page_shift));
-        return p < a.n_pages ? p : -1;
+        return j < k.n && tok < L.len ? __ldg(trow + (tok >> a.page_shift)) : kNoPage;
       };
       auto scale_at = [&](int j, int i, int page) -> float {
         const int tok = (k.blk0 + j) * BN + 64 * h + i;
-        return page < 0 ? 0.f
-                        : __ldg(a.k_scale + (static_cast<long long>(page) << a.page_shift) + (tok & ((1 << a.page_shift) - 1)));
+        return page < 0 || page >= a.n_pages ? 0.f
+                                             : __ldg(a.k_scale + (static_cast<long long>(page) << a.page_shift) + (tok & ((1 << a.page_shift) - 1)));
       };
-      bool page_next = has_page(0);
+      int entry = entry_of(0);
       float sc0 = 0.f, sc1 = 0.f;
       int pg0 = -1, pg1 = -1;
       if constexpr (KV8) {
@@ -488,8 +490,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
       for (int j = 0; j < k.n; ++j) {
         const uint32_t at = jb + j;
         const int key0 = (k.blk0 + j) * BN + 64 * h;
-        const uint32_t pages = __ballot_sync(0xffffffffu, page_next) >> (4 * h) & 0xFu;
-        page_next = has_page(j + 1);
+        const uint32_t pages = __ballot_sync(0xffffffffu, entry >= 0 && entry < a.n_pages) >> (4 * h) & 0xFu;
+        entry = entry_of(j + 1);
         if constexpr (KV8) {
           __syncwarp();
           scale_s[lane] = sc0;
