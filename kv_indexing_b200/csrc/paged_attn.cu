@@ -16,10 +16,10 @@
 //
 // A block works through the pieces of the work list (paged.cuh) that are its.
 //
-// Threads (320): warps 0-3 and 4-7 are the softmax of the two halves, one
-// thread per row; warp 8 loads K and V pages by TMA into a ring of 128-key
-// tiles (boxes of one page, or of the page's part of the block); warp 9 issues
-// the MMAs. Scores (128 columns) and O (d columns) of both halves fill tensor
+// Threads (352): warps 0-3 and 4-7 are the softmax of the two halves, one
+// thread per row; warps 8 and 10 load K and V pages by TMA into a ring of
+// 128-key tiles (boxes of one page, or of the page's part of the block; one warp
+// alone issues boxes more slowly than HBM delivers them); warp 9 issues the MMAs. Scores (128 columns) and O (d columns) of both halves fill tensor
 // memory; P (bf16) overwrites the scores it came from and is the A operand of
 // the second MMA. MMAs issued by one thread run in order, so a half's next
 // scores cannot overtake the product that reads its P.
@@ -39,7 +39,7 @@ namespace {
 using namespace paged;
 
 constexpr int kSoft = 256;             // softmax threads
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
 constexpr int BN = kPagedBN;
 
 template <int D, bool SHARED>
@@ -158,8 +158,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // place in the ring, from the piece's first tile on, of the K tile of half i's step s (its V tile follows)
   auto seq_of = [&](int i, int s) -> int { return SHARED ? 2 * s : 2 * (2 * s + i); };
 
-  if (warp == 8) {
-    // ---------------------------------------------------------- producer --
+  if (warp == 8 || warp == 10) {
+    // ------------------------------------------------ producers (K and V) --
+    const uint32_t kv = warp == 10;
     const int per = BN >> a.page_shift;        // pages of a block (page sizes up to 128)
     const int n_ops = C::kChunks * per;
     const int j = lane % per, c = lane / per;
@@ -178,25 +179,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         int page = next;
         next = page_of(blk + 1);               // not looked at before the next block: the load takes its time
         if (page < 0 || page >= a.n_pages) {
-          if (page != kNoPage && c == 0) record_bad_page(a.status);
+          if (page != kNoPage && c == 0 && kv == 0) record_bad_page(a.status);
           page = -1;
         }
         const uint32_t mapped = __ballot_sync(0xffffffffu, page >= 0) & ((1u << per) - 1u);
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++seq) {
-          const uint32_t st = seq % C::kStages;
-          ok = __all_sync(0xffffffffu, wait(&kv_empty[st], ((seq / C::kStages) & 1) ^ 1, a.status, abort_flag));
-          if (!ok) break;
-          if (lane == 0) {
-            if (kv) mask_s[st] = mapped;
-            mbar_arrive_expect_tx(&kv_full[st], C::kStage);
-          }
-          __syncwarp();
-          if (lane < n_ops)
-            tma_load_page(sStage + st * C::kStage + c * (BN * 128) + j * rows_box * 128, kv ? &tm_v : &tm_k, &kv_full[st],
-                          p.g * D + c * 64, 0, page >= 0 ? page : a.n_pages);
+        const uint32_t at = seq + 2 * blk + kv, st = at % C::kStages;
+        ok = __all_sync(0xffffffffu, wait(&kv_empty[st], ((at / C::kStages) & 1) ^ 1, a.status, abort_flag));
+        if (!ok) break;
+        if (lane == 0) {
+          if (kv) mask_s[st] = mapped;
+          mbar_arrive_expect_tx(&kv_full[st], C::kStage);
         }
+        __syncwarp();
+        if (lane < n_ops)
+          tma_load_page(sStage + st * C::kStage + c * (BN * 128) + j * rows_box * 128, kv ? &tm_v : &tm_k, &kv_full[st],
+                        p.g * D + c * 64, 0, page >= 0 ? page : a.n_pages);
       }
+      seq += 2 * n_blk;
     }
   } else if (warp == 9) {
     // -------------------------------------------------------- MMA issuer --

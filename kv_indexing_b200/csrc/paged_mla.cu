@@ -18,21 +18,25 @@
 // that measured 5.2 us a block, ten times the products themselves.)
 //
 // Per block and CTA: 128 x 128 x (576 + 512) / 2 multiply-adds (2176 cycles at
-// 4096 a cycle) against shared memory at 128 bytes a cycle: operands of Q K^T 36
-// x 4 KB, of P V 16 x 6 KB, staging 136 KB, P 16 KB: 392 KB, 3060 cycles. So
-// shared memory bounds a full pipeline, at 0.7 of the tensor rate.
+// 4096 a cycle) against shared memory at 128 bytes a cycle: operands of Q K^T
+// 12 x 4 and 24 x 2 KB, of P V 16 x 6 KB, staging 136 KB, P 16 KB: 344 KB, 2690
+// cycles. So shared memory bounds a full pipeline, at 0.8 of the tensor rate.
 //
-// Tensor memory (512 columns): O 256, S 2 x 64. Shared memory: Q 72 KB, P 2 x 16
-// KB, a ring of seven 16 KB slots. A block takes nine of them: K as 64 keys x
-// 128 columns (five, the last half empty), V as 64 keys x 128 columns (four).
-// The products of block j + 1's scores are issued before block j's P V, so the
-// tensor cores work while a block's softmax runs.
+// Tensor memory (512 columns): O 256, S 64, q's columns [0, 384) as the A operand
+// 192 (each row in lanes r and r + 64, as the pair's MMA reads it). Shared
+// memory: q's columns [384, 576) 24 KB, P 2 x 16 KB, a ring of ten 16 KB slots
+// (with all of q in shared memory there were seven, and loads came late: a block
+// took 5100 cycles). A block takes nine of them: K as 64 keys x 128 columns
+// (five, the last half empty), V as 64 keys x 128 columns (four). The scores of
+// block j + 1 are issued before block j's P V, so the tensor cores work while a
+// block's softmax runs; S is free once both CTAs hold its scores in registers.
 //
 // Threads: warps 0-3 softmax (two threads per row, 64 of the block's keys each:
-// the layout of the pair's accumulator); warp 4 loads (TMA boxes of one page, or
-// of the page's part of 64 keys); the last warp of CTA 0 issues the MMAs. e4m3:
-// warps 4-11 stage rows (codes -> bf16, exact) in place of the loads; a key's
-// scale multiplies its score and its P.
+// the layout of the pair's accumulator); warps 4-7 load every fourth slot each
+// (TMA boxes of one page, or of the page's part of 64 keys; one warp alone issues
+// boxes at 7 TB/s over the GPU, two at 13, four at 19); the last warp of CTA 0
+// issues the MMAs. e4m3: warps 4-11 stage rows (codes -> bf16, exact) in place of
+// the loads; a key's scale multiplies its score and its P.
 //
 // The running maximum moves only when a block raises it by more than 2^8 (P in
 // bf16 keeps its relative precision, sums are fp32), so O is rescaled rarely.
@@ -54,16 +58,17 @@ constexpr int BN = kPagedBN;
 constexpr int kRows = 128;                       // rows of a tile, 64 per CTA
 constexpr int kChunk = 64 * 128;                 // 64 keys (or rows) x 64 columns, bytes
 constexpr int kSlot = 2 * kChunk;
-constexpr int kSlots = 7;
+constexpr int kSlots = 10;
 constexpr int kPBytes = 2 * kChunk;              // 64 rows x 128 keys
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColO = 0, kColS = 256;
-constexpr int kOffP = 9 * kChunk;
+constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
+constexpr int kTmemChunks = 6;                   // 64-column chunks of q in tensor memory, the rest in shared memory
+constexpr int kOffP = (9 - kTmemChunks) * kChunk;
 constexpr int kOffRing = kOffP + 2 * kPBytes;
 constexpr int kOffTag = kOffRing + kSlots * kSlot;   // [2][128] u64 tagged maxima, [128] u64 tagged sums
 constexpr int kOffScale = kOffTag + 3 * 128 * 8;     // e4m3: [4 warps][64] scales of the block's keys
 constexpr int kOffBars = kOffScale + 4 * 64 * 4;
-constexpr int kNumBars = 2 * kSlots + 8;
+constexpr int kNumBars = 2 * kSlots + 11;   // full, empty, s_full, s_free, p_full[2], pv_done, o_full, q_full, tail[4]
 constexpr int kOffWork = kOffBars + kNumBars * 8;
 constexpr int kOffMisc = kOffWork + sizeof(Work);
 constexpr size_t kSmem = 1024 + kOffMisc + 16;
@@ -91,16 +96,21 @@ __device__ __forceinline__ bool get_tagged(const volatile unsigned long long* sl
   return true;
 }
 
-// e4m3 pair -> bf16 pair, exact.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t two_codes) {
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(two_codes)));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-  return pack_bf16(f.x, f.y);
+// Two of four e4m3 codes (the lower or the upper pair) -> a bf16 pair, exact:
+// the code's exponent and mantissa, moved to the low end of bf16's exponent and
+// the high end of its mantissa, are the value times 2^-120 (bias 127 against 7),
+// subnormal codes included.
+template <int HIGH>
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t four) {
+  const uint32_t x = __byte_perm(four, 0u, HIGH ? 0x3424 : 0x1404);   // each code in the high byte of a half
+  const uint32_t bits = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(bits), "r"(0x7B807B80u));   // 2^120
+  return r;
 }
 
 template <bool KV8>
-constexpr int threads_of() { return KV8 ? 416 : 192; }
+constexpr int threads_of() { return KV8 ? 416 : 288; }
 
 template <bool KV8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1)
@@ -114,16 +124,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
   volatile unsigned long long* tag_sum = tag_max + 2 * 128;
   uint64_t* full = reinterpret_cast<uint64_t*>(base + kOffBars);   // CTA 0: both halves of a slot are there
   uint64_t* empty = full + kSlots;
-  uint64_t* s_full = empty + kSlots;   // [2]
-  uint64_t* p_full = s_full + 2;       // [2], CTA 0: P of both CTAs is stored
+  uint64_t* s_full = empty + kSlots;
+  uint64_t* s_free = s_full + 1;       // CTA 0: both CTAs have read the scores
+  uint64_t* p_full = s_free + 1;       // [2], CTA 0: P of both CTAs is stored
   uint64_t* pv_done = p_full + 2;
   uint64_t* o_full = pv_done + 1;      // the piece's last product
   uint64_t* q_full = o_full + 1;       // CTA 0
-  uint64_t* tail = q_full + 1;         // a slot that is cleared in part before it counts
+  uint64_t* tail = q_full + 1;         // [4] a slot that is cleared in part before it counts, by loading warp
   Work* work_s = reinterpret_cast<Work*>(base + kOffWork);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  constexpr int kMmaWarp = KV8 ? 12 : 5;
+  constexpr int kMmaWarp = KV8 ? 12 : 8;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -135,14 +146,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
       mbar_init(&full[i], KV8 ? 16 : 2);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 8);
-    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 8);
+    for (int i = 0; i < 2; ++i) mbar_init(&p_full[i], 8);
     mbar_init(pv_done, 1);
     mbar_init(o_full, 1);
     mbar_init(q_full, 8);
-    mbar_init(tail, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&tail[i], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -159,89 +169,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
   cluster_sync_all();   // the partner's barriers are initialised before any remote arrive
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const uint32_t tO = tmem + kColO, tS = tmem + kColS;
+  const uint32_t tO = tmem + kColO, tS = tmem + kColS, tQ = tmem + kColQ;
   const uint32_t full0 = mapa_shared(smem_u32(full), 0);         // CTA 0's barriers
   bool ok = true;
 
   if (warp == kMmaWarp) {
     // ---------------------------------------------------------- MMA issuer --
-    if (rank == 0) {
+    // One thread. A barrier is looked at while the products before it are
+    // issued: waiting for each in turn, with the products in between, took
+    // longer (3700 cycles a block) than the products themselves.
+    if (rank == 0 && elect_one()) {
       const uint32_t idesc_qk = make_idesc(1, 1, 128, BN, 0, 0);
       const uint32_t idesc_pv = make_idesc(1, 1, 128, 256, 0, 1);
       const uint64_t dQ = make_sdesc(smem_u32(sQ), 16, 1024, kLayoutSW128);
       const uint64_t dP = make_sdesc(smem_u32(sP), 16, 1024, kLayoutSW128);
       const uint64_t dK = make_sdesc(smem_u32(sRing), 16, 1024, kLayoutSW128);
       const uint64_t dV = make_sdesc(smem_u32(sRing), kChunk, 1024, kLayoutSW128);
-      int st = 0;                      // slot of the ring and the parity of its phase
+      int st = 0, cur;                 // the ring's next slot and the parity of its phase; the slot at hand
       uint32_t ph = 0;
-      auto advance = [&] {
+      bool seen = false;               // the next slot has been seen full
+      // Waits for the next slot, makes it the current one and looks at the one after.
+      auto take = [&]() -> bool {
+        if (!seen && !wait(&full[st], ph, a.status, abort_flag)) return false;
+        cur = st;
         if (++st == kSlots) {
           st = 0;
           ph ^= 1u;
         }
+        seen = mbar_test_wait(&full[st], ph);
+        tc_fence_after();
+        return true;
       };
       uint32_t jb = 0, seg = 0;        // blocks and pieces so far
+      bool seen_p = false, seen_s = false;
       auto qk = [&](uint32_t j) -> bool {
-#pragma unroll 1
-        for (int s = 0; s < 5; ++s) {
-          if (!wait(&full[st], ph, a.status, abort_flag)) return false;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t q0 = dQ + s * (kSlot / 16), k0 = dK + st * (kSlot / 16);
-            const uint32_t d = tS + 64 * (j & 1);
+        if (j > 0 && !seen_s && !wait(s_free, (j - 1) & 1, a.status, abort_flag)) return false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) umma_f16_pair(d, q0 + 2 * i, k0 + 2 * i, idesc_qk, (s | i) ? 1u : 0u);
-            if (s < 4) {
+        for (int s = 0; s < 5; ++s) {        // columns [128 s, 128 s + 128)
+          if (!take()) return false;
+          const uint64_t k0 = dK + cur * (kSlot / 16);
+          if (s == 4) seen_p = j > 0 && mbar_test_wait(&p_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                umma_f16_pair(d, q0 + kChunk / 16 + 2 * i, k0 + kChunk / 16 + 2 * i, idesc_qk, 1u);
+          for (int c = 0; c < (s < 4 ? 2 : 1); ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint64_t kd = k0 + c * (kChunk / 16) + 2 * i;
+              if (2 * s + c < kTmemChunks)
+                umma_f16_ts_pair(tS, tQ + (2 * s + c) * 32 + 8 * i, kd, idesc_qk, (s | c | i) ? 1u : 0u);
+              else
+                umma_f16_pair(tS, dQ + (2 * s + c - kTmemChunks) * (kChunk / 16) + 2 * i, kd, idesc_qk, 1u);
             }
-            umma_commit_pair(&empty[st]);
-            if (s == 4) umma_commit_pair(&s_full[j & 1]);
-          }
-          __syncwarp();
-          advance();
+          umma_commit_pair(&empty[cur]);
         }
+        umma_commit_pair(s_full);
         return true;
       };
       auto pv = [&](uint32_t j, bool first, bool last) -> bool {
-        if (!wait(&p_full[j & 1], (j >> 1) & 1, a.status, abort_flag)) return false;
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {        // (half of the keys, half of the columns)
-          if (!wait(&full[st], ph, a.status, abort_flag)) return false;
-          tc_fence_after();
-          if (elect_one()) {
-            const int h = i >> 1, n = i & 1;
-            const uint64_t p0 = dP + ((j & 1) * kPBytes + h * kChunk) / 16, v0 = dV + st * (kSlot / 16);
+        if (!seen_p && !wait(&p_full[j & 1], (j >> 1) & 1, a.status, abort_flag)) return false;
+        seen_p = false;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_f16_pair(tO + n * 128, p0 + 2 * ks, v0 + 128 * ks, idesc_pv, first && h == 0 && ks == 0 ? 0u : 1u);
-            umma_commit_pair(&empty[st]);
-            if (i == 3) umma_commit_pair(pv_done);
-            if (i == 3 && last) umma_commit_pair(o_full);
-          }
-          __syncwarp();
-          advance();
+        for (int i = 0; i < 4; ++i) {        // (half of the keys, half of the columns)
+          if (!take()) return false;
+          const int h = i >> 1, n = i & 1;
+          const uint64_t p0 = dP + ((j & 1) * kPBytes + h * kChunk) / 16, v0 = dV + cur * (kSlot / 16);
+          if (i == 3) seen_s = !last && mbar_test_wait(s_free, (j + 1) & 1);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16_pair(tO + n * 128, p0 + 2 * ks, v0 + 128 * ks, idesc_pv, first && h == 0 && ks == 0 ? 0u : 1u);
+          umma_commit_pair(&empty[cur]);
         }
+        umma_commit_pair(pv_done);
+        if (last) umma_commit_pair(o_full);
         return true;
       };
       for (Work k = *work_s; ok && k.n > 0; next_work<kRows, BN>(a, k), ++seg) {
         ok = wait(q_full, seg & 1, a.status, abort_flag) && qk(jb);
+        seen_p = false;                      // (of the piece before)
         for (int j = 0; ok && j < k.n; ++j) {
           if (j + 1 < k.n) ok = qk(jb + j + 1);
           if (ok) ok = pv(jb + j, j == 0, j + 1 == k.n);
         }
         jb += k.n;
+        seen_s = false;
       }
     }
+    __syncwarp();
   } else if (warp >= 4) {
     if constexpr (!KV8) {
       // -------------------------------------------------------- producer --
       const int box = min(kPagedBox, 1 << a.page_shift);         // rows of a box
       const int per = 64 / box;                                  // boxes of 64 keys
       const int c = lane / per, i = lane - c * per;              // this lane's box: chunk c, rows i * box
+      const uint32_t pw = warp - 4;
+      uint64_t* my_tail = tail + pw;
       int st = 0;
-      uint32_t ph = 1, n_tail = 0;                               // the ring starts empty
+      uint32_t ph = 1, seq = 0, n_tail = 0;                      // the ring starts empty
       for (Work k = *work_s; ok && k.n > 0; next_work<kRows, BN>(a, k)) {
         const int b = k.bt / a.tiles;
         const Lens L = lens_of(a, b);
@@ -253,32 +275,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
         };
         auto page_of = [&](int p) -> int {
           if (p >= 0 && p < a.n_pages) return p;
-          if (p != kNoPage) record_bad_page(a.status);
+          if (p != kNoPage && pw == 0) record_bad_page(a.status);
           return -1;
         };
         // a slot: 64 keys from `key` of block j, `nc` chunks of columns from `chunk`
         auto load = [&](int j, int pages, int key, int chunk, int nc, bool is_v) -> bool {
-          if (!__all_sync(0xffffffffu, wait(&empty[st], ph, a.status, abort_flag))) return false;
+          const int at = st;
+          const uint32_t parity = ph;
+          if (++st == kSlots) {
+            st = 0;
+            ph ^= 1u;
+          }
+          if ((seq++ & 3u) != pw) return true;                   // another warp's
+          if (!__all_sync(0xffffffffu, wait(&empty[at], parity, a.status, abort_flag))) return false;
           const int tok = (k.blk0 + j) * BN + key;
           const int page = __shfl_sync(0xffffffffu, pages, ((key + i * box) >> 4) & 31);
           const int rows = L.len - tok;                          // rows that hold a token
           const bool clear = is_v && rows > 0 && rows < 64;
           if (lane == 0) {
-            if (clear) mbar_arrive_expect_tx(tail, nc * kChunk);
-            else mbar_arrive_expect_tx_at(full0 + st * 8, nc * kChunk);
+            if (clear) mbar_arrive_expect_tx(my_tail, nc * kChunk);
+            else mbar_arrive_expect_tx_at(full0 + at * 8, nc * kChunk);
           }
           __syncwarp();
-          uint8_t* dst = sRing + st * kSlot;
+          uint8_t* dst = sRing + at * kSlot;
           if (lane < nc * per) {
             const int in_page = (tok + i * box) & ((1 << a.page_shift) - 1);
             if (clear)
-              tma_load_page(dst + c * kChunk + i * box * 128, &tm_k, tail, (chunk + c) * 64, in_page, page >= 0 ? page : a.n_pages);
+              tma_load_page(dst + c * kChunk + i * box * 128, &tm_k, my_tail, (chunk + c) * 64, in_page, page >= 0 ? page : a.n_pages);
             else
-              tma_load_page_pair(dst + c * kChunk + i * box * 128, &tm_k, full0 + st * 8, (chunk + c) * 64, in_page,
+              tma_load_page_pair(dst + c * kChunk + i * box * 128, &tm_k, full0 + at * 8, (chunk + c) * 64, in_page,
                                  page >= 0 ? page : a.n_pages);
           }
           if (clear) {
-            if (!__all_sync(0xffffffffu, wait(tail, n_tail & 1, a.status, abort_flag))) return false;
+            if (!__all_sync(0xffffffffu, wait(my_tail, n_tail & 1, a.status, abort_flag))) return false;
             ++n_tail;
             for (int z = lane; z < (64 - rows) * 16; z += 32) {
               const int zr = rows + (z >> 4), u = z & 15;
@@ -286,11 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive_at(full0 + st * 8);
-          }
-          if (++st == kSlots) {
-            st = 0;
-            ph ^= 1u;
+            if (lane == 0) mbar_arrive_at(full0 + at * 8);
           }
           return true;
         };
@@ -316,74 +341,77 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
       }
     } else {
       // --------------------------------------------- e4m3: stage the rows --
-      // Four threads per key, each a quarter of a slot's columns. K's codes of
-      // a block are loaded while V's of the last one are converted, and the
-      // other way round.
+      // A slot's 64 rows x 128 codes are read 16 bytes a lane, eight lanes to a
+      // row (a chunk alone: four). K's codes of a block are loaded while V's of
+      // the last one are converted, and the other way round.
       const int t = tid - 128;
-      const int row = t & 63, part = t >> 6;
+      const int row = t >> 3, piece = t & 7;       // rows `row` and `row` + 32
+      const int row8 = t >> 2, piece8 = t & 3;     // chunk 8
       int st = 0;
       uint32_t ph = 1;
       for (Work k = *work_s; ok && k.n > 0; next_work<kRows, BN>(a, k)) {
         const int b = k.bt / a.tiles;
         const Lens L = lens_of(a, b);
         const int* trow = a.table + static_cast<long long>(b) * a.max_pages;
-        // the table entry of this thread's key in half h of block j; looked at a block later
-        auto entry_of = [&](int j, int h) -> int {
-          const int tok = (k.blk0 + j) * BN + h * 64 + row;
-          return j < k.n && tok < L.len ? __ldg(trow + (tok >> a.page_shift)) : kNoPage;
+        // lane g < 8: the table entry of the block's keys [16 g, 16 g + 16); looked at a block later
+        auto entry_of = [&](int j) -> int {
+          const int tok = (k.blk0 + j) * BN + lane * 16;
+          return lane < 8 && j < k.n && tok < L.len ? __ldg(trow + (tok >> a.page_shift)) : kNoPage;
         };
         auto page_of = [&](int p) -> int {
           if (p >= 0 && p < a.n_pages) return p;
-          if (p != kNoPage && part == 0) record_bad_page(a.status);
+          if (p != kNoPage && warp == 4) record_bad_page(a.status);
           return -1;
         };
-        auto row_of = [&](int j, int h, int page) -> const uint4* {
-          const int tok = (k.blk0 + j) * BN + h * 64 + row;
+        // row `key` of block j, or null where nothing is to be read
+        auto row_of = [&](int j, int pages, int key) -> const uint4* {
+          const int page = __shfl_sync(0xffffffffu, pages, key >> 4);
+          const int tok = (k.blk0 + j) * BN + key;
+          if (page < 0 || tok >= L.len) return nullptr;
           return reinterpret_cast<const uint4*>(a.kv8 + page * a.kv8_page + (tok & ((1 << a.page_shift) - 1)) * a.kv8_row);
         };
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         uint4 vk[9], vv[8];
-        auto load_k = [&](int j, int page) {
-          if (page < 0) {
-#pragma unroll
-            for (int i = 0; i < 9; ++i) vk[i] = zero;
-            return;
-          }
-          const uint4* src = row_of(j, rank, page);
+        auto load_k = [&](int j, int pages) {
+          const uint4* r0 = row_of(j, pages, rank * 64 + row);
+          const uint4* r1 = row_of(j, pages, rank * 64 + row + 32);
+          const uint4* r8 = row_of(j, pages, rank * 64 + row8);
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            vk[2 * s] = __ldg(src + s * 8 + part * 2);
-            vk[2 * s + 1] = __ldg(src + s * 8 + part * 2 + 1);
+            vk[2 * s] = r0 ? __ldg(r0 + s * 8 + piece) : zero;
+            vk[2 * s + 1] = r1 ? __ldg(r1 + s * 8 + piece) : zero;
           }
-          vk[8] = __ldg(src + 32 + part);
+          vk[8] = r8 ? __ldg(r8 + 32 + piece8) : zero;
         };
-        auto load_v = [&](int j, int page0, int page1) {
+        auto load_v = [&](int j, int pages) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int page = h ? page1 : page0;
-            const uint4* src = page >= 0 ? row_of(j, h, page) + rank * 8 + part * 2 : nullptr;
+            const uint4* r0 = row_of(j, pages, h * 64 + row);
+            const uint4* r1 = row_of(j, pages, h * 64 + row + 32);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-              vv[4 * h + 2 * n] = src ? __ldg(src + n * 16) : zero;
-              vv[4 * h + 2 * n + 1] = src ? __ldg(src + n * 16 + 1) : zero;
+              vv[4 * h + 2 * n] = r0 ? __ldg(r0 + n * 16 + rank * 8 + piece) : zero;
+              vv[4 * h + 2 * n + 1] = r1 ? __ldg(r1 + n * 16 + rank * 8 + piece) : zero;
             }
           }
         };
-        auto put = [&](uint8_t* chunk, int unit, const uint4& e) {   // 16 codes -> two 16-byte units of a chunk's row
-          uint8_t* dst = chunk + row * 128;
-          *reinterpret_cast<uint4*>(dst + ((unit ^ (row & 7)) << 4)) =
-              make_uint4(e4m3x2_to_bf16x2(e.x), e4m3x2_to_bf16x2(e.x >> 16), e4m3x2_to_bf16x2(e.y), e4m3x2_to_bf16x2(e.y >> 16));
-          *reinterpret_cast<uint4*>(dst + (((unit + 1) ^ (row & 7)) << 4)) =
-              make_uint4(e4m3x2_to_bf16x2(e.z), e4m3x2_to_bf16x2(e.z >> 16), e4m3x2_to_bf16x2(e.w), e4m3x2_to_bf16x2(e.w >> 16));
+        // 16 codes -> two 16-byte units of a chunk's row; `flip`: the upper one first, so that the lanes of two chunks
+        // do not meet in a bank
+        auto put = [&](uint8_t* chunk, int r, int unit, const uint4& e, bool flip) {
+          uint8_t* dst = chunk + r * 128;
+          const uint4 lo = make_uint4(codes_to_bf16<0>(e.x), codes_to_bf16<1>(e.x), codes_to_bf16<0>(e.y), codes_to_bf16<1>(e.y));
+          const uint4 hi = make_uint4(codes_to_bf16<0>(e.z), codes_to_bf16<1>(e.z), codes_to_bf16<0>(e.w), codes_to_bf16<1>(e.w));
+          *reinterpret_cast<uint4*>(dst + (((unit + flip) ^ (r & 7)) << 4)) = flip ? hi : lo;
+          *reinterpret_cast<uint4*>(dst + (((unit + !flip) ^ (r & 7)) << 4)) = flip ? lo : hi;
         };
         auto emit = [&](const uint4& e0, const uint4& e1, bool two) -> bool {
           if (!__all_sync(0xffffffffu, wait(&empty[st], ph, a.status, abort_flag))) return false;
           uint8_t* dst = sRing + st * kSlot;
           if (two) {
-            put(dst + (part >> 1) * kChunk, (part & 1) * 4, e0);
-            put(dst + (part >> 1) * kChunk, (part & 1) * 4 + 2, e1);
+            put(dst + (piece >> 2) * kChunk, row, (piece & 3) * 2, e0, piece >> 2);
+            put(dst + (piece >> 2) * kChunk, row + 32, (piece & 3) * 2, e1, piece >> 2);
           } else {
-            put(dst, part * 2, e0);
+            put(dst, row8, piece8 * 2, e0, row8 & 1);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -406,30 +434,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
             if (!emit(vv[2 * s], vv[2 * s + 1], true)) return false;
           return true;
         };
-        // pages of block j + 1, entries of block j + 2 (both halves of the keys)
-        int n0 = page_of(entry_of(0, 0)), n1 = page_of(entry_of(0, 1));
-        int e0 = entry_of(1, 0), e1 = entry_of(1, 1);
-        load_k(0, rank ? n1 : n0);
-        load_v(0, n0, n1);
-        n0 = page_of(e0);
-        n1 = page_of(e1);
-        e0 = entry_of(2, 0);
-        e1 = entry_of(2, 1);
+        int pages = page_of(entry_of(0));
+        int entry = entry_of(1);
+        load_k(0, pages);
+        load_v(0, pages);
+        int next = page_of(entry);
+        entry = entry_of(2);
         ok = emit_k();
-        load_k(1, rank ? n1 : n0);
+        load_k(1, next);
         for (int j = 0; ok && j < k.n; ++j) {
-          const int m0 = page_of(e0), m1 = page_of(e1);
-          e0 = entry_of(j + 3, 0);
-          e1 = entry_of(j + 3, 1);
+          const int after = page_of(entry);
+          entry = entry_of(j + 3);
           if (j + 1 < k.n) {
             ok = emit_k();
             if (!ok) break;
           }
-          load_k(j + 2, rank ? m1 : m0);
+          load_k(j + 2, after);
           ok = emit_v();
-          load_v(j + 1, n0, n1);
-          n0 = m0;
-          n1 = m1;
+          load_v(j + 1, next);
+          next = after;
         }
       }
     }
@@ -438,6 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
     const int h = tid >> 6, r = tid & 63;          // half of the block's keys, row of the CTA
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t p_full0 = mapa_shared(smem_u32(p_full), 0), q_full0 = mapa_shared(smem_u32(q_full), 0);
+    const uint32_t s_free0 = mapa_shared(smem_u32(s_free), 0);
     float* scale_s = reinterpret_cast<float*>(base + kOffScale) + warp * 64;
     const float c = a.scale_log2;
     uint32_t jb = 0, seg = 0;
@@ -448,15 +472,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
       const int* trow = a.table + static_cast<long long>(b) * a.max_pages;
       const long long q0 = static_cast<long long>(b) * a.T * a.Hq + row0;   // the CTA's first row of q and out
       {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + q0 * 576);
-        const int live = (rows - row0) * 72;       // 16-byte units that exist
-#pragma unroll 9
-        for (int i = tid; i < 64 * 72; i += 128) {
-          const int rr = i / 72, u = i - rr * 72;
-          const uint4 v = i < live ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(sQ + (u >> 3) * kChunk + rr * 128 + (((u & 7) ^ (rr & 7)) << 4)) = v;
+        const bool mine = row0 + r < rows;
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (q0 + r) * 576);
+#pragma unroll 2
+        for (int ch = 0; ch < kTmemChunks; ++ch) {     // two bf16 per column, ascending; both threads of a row
+          uint32_t v[32];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const uint4 w = mine ? __ldg(src + ch * 8 + u) : make_uint4(0u, 0u, 0u, 0u);
+            v[4 * u] = w.x;
+            v[4 * u + 1] = w.y;
+            v[4 * u + 2] = w.z;
+            v[4 * u + 3] = w.w;
+          }
+          tmem_st32(tQ + lane_base + ch * 32, v);
         }
+#pragma unroll
+        for (int u = h; u < (9 - kTmemChunks) * 8; u += 2) {
+          const uint4 w = mine ? __ldg(src + kTmemChunks * 8 + u) : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(sQ + (u >> 3) * kChunk + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = w;
+        }
+        tmem_st_wait();
         fence_proxy_async_smem();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_at(q_full0);
       }
@@ -502,15 +540,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
           pg0 = page_at(j + 2, lane);
           pg1 = page_at(j + 2, lane + 32);
         }
-        ok = __all_sync(0xffffffffu, wait(&s_full[at & 1], (at >> 1) & 1, a.status, abort_flag));
+        ok = __all_sync(0xffffffffu, wait(s_full, at & 1, a.status, abort_flag));
         if (!ok) break;
         tc_fence_after();
         float x[64];
         {
           uint32_t s0[32], s1[32];
-          tmem_ld32(tS + lane_base + 64 * (at & 1), s0);
-          tmem_ld32(tS + lane_base + 64 * (at & 1) + 32, s1);
+          tmem_ld32(tS + lane_base, s0);
+          tmem_ld32(tS + lane_base + 32, s1);
           tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_at(s_free0);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             x[i] = __uint_as_float(s0[i]);
