@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mask(v1, q + 1);
           }
 #pragma unroll
-          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], fmaxf(__uint_as_float(v0[j]), __uint_as_float(v1[j])));
+          for (int j = 0; j < 32; ++j) mx[j & 3] = max3(mx[j & 3], __uint_as_float(v0[j]), __uint_as_float(v1[j]));
         }
       }
       const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       const float mu = m_run == -INFINITY ? 0.f : m_run;   // all masked so far: exp2(-inf) = 0
-      float ps[4] = {0.f, 0.f, 0.f, 0.f};
+      float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      const float2 c2 = make_float2(c, c), mu2 = make_float2(-mu, -mu);
       {
         uint32_t v[2][32];
         tmem_ld32(tS, v[0]);
@@ -398,15 +399,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float p0 = ex2(fmaf(__uint_as_float(x[2 * j]), c, -mu));
-            const float p1 = ex2(fmaf(__uint_as_float(x[2 * j + 1]), c, -mu));
-            ps[j & 3] += p0 + p1;
-            pk[j] = pack_bf16(p0, p1);
+            float2 p = fma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), c2, mu2);
+            p.x = ex2(p.x);
+            p.y = ex2(p.y);
+            ps[j & 1] = add2(ps[j & 1], p);
+            pk[j] = pack_bf16(p.x, p.y);
           }
           tmem_st16(tS + 16 * q, pk);           // over scores that have been read
         }
       }
-      l_run += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+      l_run += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
       clear_tail(seq_v, key0);
       tmem_st_wait();
       tc_fence_before();

@@ -65,36 +65,15 @@ constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 constexpr int kTmemChunks = 6;                   // 64-column chunks of q in tensor memory, the rest in shared memory
 constexpr int kOffP = (9 - kTmemChunks) * kChunk;
 constexpr int kOffRing = kOffP + 2 * kPBytes;
-constexpr int kOffTag = kOffRing + kSlots * kSlot;   // [2][128] u64 tagged maxima, [128] u64 tagged sums
-constexpr int kOffScale = kOffTag + 3 * 128 * 8;     // e4m3: [4 warps][64] scales of the block's keys
+constexpr int kOffSwap = kOffRing + kSlots * kSlot;  // [2][128] what a row's two threads tell each other
+constexpr int kOffScale = kOffSwap + 2 * 128 * 4;     // e4m3: [4 warps][64] scales of the block's keys
 constexpr int kOffBars = kOffScale + 4 * 64 * 4;
-constexpr int kNumBars = 2 * kSlots + 11;   // full, empty, s_full, s_free, p_full[2], pv_done, o_full, q_full, tail[4]
+constexpr int kNumBars = 2 * kSlots + 13;   // full, empty, s_full, s_free, p_full[2], pv_done, o_full, q_full, tail[4], swap[2]
 constexpr int kOffWork = kOffBars + kNumBars * 8;
 constexpr int kOffMisc = kOffWork + sizeof(Work);
 constexpr size_t kSmem = 1024 + kOffMisc + 16;
 static_assert(kOffRing % 1024 == 0 && kOffScale % 16 == 0 && kOffBars % 8 == 0 && kOffWork % 8 == 0 && kSmem <= 227 * 1024,
               "shared memory layout");
-
-__device__ __forceinline__ void put_tagged(volatile unsigned long long* slot, uint32_t tag, float v) {
-  *slot = (static_cast<unsigned long long>(tag) << 32) | __float_as_uint(v);
-}
-__device__ __forceinline__ bool get_tagged(const volatile unsigned long long* slot, uint32_t tag, float* v,
-                                           int* status, volatile int* abort_flag) {
-  unsigned long long x = *slot;
-  if (static_cast<uint32_t>(x >> 32) != tag) {
-    const long long t0 = clock64();
-    while (static_cast<uint32_t>((x = *slot) >> 32) != tag) {
-      if (*abort_flag) return false;
-      if (clock64() - t0 > kWaitLimitCycles) {
-        record_timeout(status);
-        *abort_flag = 1;
-        return false;
-      }
-    }
-  }
-  *v = __uint_as_float(static_cast<uint32_t>(x));
-  return true;
-}
 
 // Two of four e4m3 codes (the lower or the upper pair) -> a bf16 pair, exact:
 // the code's exponent and mantissa, moved to the low end of bf16's exponent and
@@ -120,8 +99,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
   uint8_t* sQ = base;
   uint8_t* sP = base + kOffP;
   uint8_t* sRing = base + kOffRing;
-  volatile unsigned long long* tag_max = reinterpret_cast<volatile unsigned long long*>(base + kOffTag);
-  volatile unsigned long long* tag_sum = tag_max + 2 * 128;
+  float* swap_s = reinterpret_cast<float*>(base + kOffSwap);
   uint64_t* full = reinterpret_cast<uint64_t*>(base + kOffBars);   // CTA 0: both halves of a slot are there
   uint64_t* empty = full + kSlots;
   uint64_t* s_full = empty + kSlots;
@@ -131,6 +109,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
   uint64_t* o_full = pv_done + 1;      // the piece's last product
   uint64_t* q_full = o_full + 1;       // CTA 0
   uint64_t* tail = q_full + 1;         // [4] a slot that is cleared in part before it counts, by loading warp
+  uint64_t* swap = tail + 4;           // [2] warps w and w + 2 have stored theirs
   Work* work_s = reinterpret_cast<Work*>(base + kOffWork);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -153,10 +132,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
     mbar_init(o_full, 1);
     mbar_init(q_full, 8);
     for (int i = 0; i < 4; ++i) mbar_init(&tail[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&swap[i], 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  for (int i = tid; i < 3 * 128; i += threads_of<KV8>()) tag_max[i] = 0ull;   // 0 is never a live tag
   if (warp == kMmaWarp) tmem_alloc_pair(tmem_slot, kTmemCols);
   pdl_wait();
   pdl_trigger();
@@ -181,10 +160,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
     if (rank == 0 && elect_one()) {
       const uint32_t idesc_qk = make_idesc(1, 1, 128, BN, 0, 0);
       const uint32_t idesc_pv = make_idesc(1, 1, 128, 256, 0, 1);
-      const uint64_t dQ = make_sdesc(smem_u32(sQ), 16, 1024, kLayoutSW128);
-      const uint64_t dP = make_sdesc(smem_u32(sP), 16, 1024, kLayoutSW128);
-      const uint64_t dK = make_sdesc(smem_u32(sRing), 16, 1024, kLayoutSW128);
-      const uint64_t dV = make_sdesc(smem_u32(sRing), kChunk, 1024, kLayoutSW128);
+      const uint32_t hi = static_cast<uint32_t>(make_sdesc(0, 16, 1024, kLayoutSW128) >> 32);
+      const uint32_t dQ = static_cast<uint32_t>(make_sdesc(smem_u32(sQ), 16, 1024, kLayoutSW128));
+      const uint32_t dP = static_cast<uint32_t>(make_sdesc(smem_u32(sP), 16, 1024, kLayoutSW128));
+      const uint32_t dK = static_cast<uint32_t>(make_sdesc(smem_u32(sRing), 16, 1024, kLayoutSW128));
+      const uint32_t dV = static_cast<uint32_t>(make_sdesc(smem_u32(sRing), kChunk, 1024, kLayoutSW128));
       int st = 0, cur;                 // the ring's next slot and the parity of its phase; the slot at hand
       uint32_t ph = 0;
       bool seen = false;               // the next slot has been seen full
@@ -207,17 +187,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
 #pragma unroll
         for (int s = 0; s < 5; ++s) {        // columns [128 s, 128 s + 128)
           if (!take()) return false;
-          const uint64_t k0 = dK + cur * (kSlot / 16);
+          const uint32_t k0 = dK + cur * (kSlot / 16);
           if (s == 4) seen_p = j > 0 && mbar_test_wait(&p_full[(j - 1) & 1], ((j - 1) >> 1) & 1);
 #pragma unroll
           for (int c = 0; c < (s < 4 ? 2 : 1); ++c)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const uint64_t kd = k0 + c * (kChunk / 16) + 2 * i;
+              const uint32_t kd = k0 + c * (kChunk / 16) + 2 * i;
               if (2 * s + c < kTmemChunks)
-                umma_f16_ts_pair(tS, tQ + (2 * s + c) * 32 + 8 * i, kd, idesc_qk, (s | c | i) ? 1u : 0u);
+                umma_f16_ts_pair(tS, tQ + (2 * s + c) * 32 + 8 * i, kd, hi, idesc_qk, (s | c | i) ? 1u : 0u);
               else
-                umma_f16_pair(tS, dQ + (2 * s + c - kTmemChunks) * (kChunk / 16) + 2 * i, kd, idesc_qk, 1u);
+                umma_f16_pair(tS, dQ + (2 * s + c - kTmemChunks) * (kChunk / 16) + 2 * i, kd, hi, idesc_qk, 1u);
             }
           umma_commit_pair(&empty[cur]);
         }
@@ -231,11 +211,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
         for (int i = 0; i < 4; ++i) {        // (half of the keys, half of the columns)
           if (!take()) return false;
           const int h = i >> 1, n = i & 1;
-          const uint64_t p0 = dP + ((j & 1) * kPBytes + h * kChunk) / 16, v0 = dV + cur * (kSlot / 16);
+          const uint32_t p0 = dP + ((j & 1) * kPBytes + h * kChunk) / 16, v0 = dV + cur * (kSlot / 16);
           if (i == 3) seen_s = !last && mbar_test_wait(s_free, (j + 1) & 1);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            umma_f16_pair(tO + n * 128, p0 + 2 * ks, v0 + 128 * ks, idesc_pv, first && h == 0 && ks == 0 ? 0u : 1u);
+            umma_f16_pair(tO + n * 128, p0 + 2 * ks, v0 + 128 * ks, hi, idesc_pv, first && h == 0 && ks == 0 ? 0u : 1u);
           umma_commit_pair(&empty[cur]);
         }
         umma_commit_pair(pv_done);
@@ -464,7 +444,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
     const uint32_t s_free0 = mapa_shared(smem_u32(s_free), 0);
     float* scale_s = reinterpret_cast<float*>(base + kOffScale) + warp * 64;
     const float c = a.scale_log2;
-    uint32_t jb = 0, seg = 0;
+    uint32_t jb = 0, seg = 0, n_swap = 0;
+    // Tells the row's other thread v and returns its value (through alternate buffers: a value is read before the
+    // partner can get to the exchange after the next).
+    auto exchange = [&](float v, float* other) -> bool {
+      float* buf = swap_s + (n_swap & 1) * 128;
+      buf[tid] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&swap[warp & 1]);
+      const bool done = __all_sync(0xffffffffu, wait(&swap[warp & 1], n_swap & 1, a.status, abort_flag));
+      ++n_swap;
+      *other = buf[tid ^ 64];
+      return done;
+    };
     for (Work k = *work_s; ok && k.n > 0; next_work<kRows, BN>(a, k), ++seg) {
       const int b = k.bt / a.tiles, row0 = (k.bt - b * a.tiles) * kRows + rank * 64;
       const Lens L = lens_of(a, b);
@@ -575,14 +567,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
           for (int i = 0; i < 64; ++i)
             if (i >= vis || !((pages >> (i >> 4)) & 1u)) x[i] = -INFINITY;
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int i = 0; i < 64; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
-        const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-        // the row's other half: the partner is at the same block, one block's slots are read before they are written again
-        put_tagged(tag_max + (at & 1) * 128 + tid, at + 1, mine);
+        for (int i = 4; i < 60; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], x[i + e], x[i + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[60 + e]);
+        const float mine = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
         float other;
-        ok = __all_sync(0xffffffffu, get_tagged(tag_max + (at & 1) * 128 + (tid ^ 64), at + 1, &other, a.status, abort_flag));
+        ok = exchange(mine, &other);
         if (!ok) break;
         const float mb = fmaxf(mine, other);
         const bool move = mb > m_run + 8.f || (m_run == -INFINITY && mb != -INFINITY);
@@ -595,25 +589,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
         const float mu = m_run == -INFINITY ? 0.f : m_run;   // all masked so far: exp2(-inf) = 0
         // P of block at - 2 has been read: its product was issued before the scores of this block
         uint8_t* prow = sP + (at & 1) * kPBytes + h * kChunk + r * 128;
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 c2 = make_float2(c, c), mu2 = make_float2(-mu, -mu);
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           uint32_t w[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = 8 * u + 2 * e;
-            float p0 = ex2(fmaf(x[i], c, -mu)), p1 = ex2(fmaf(x[i + 1], c, -mu));
-            ps[e] += p0 + p1;
+            float2 p = fma2(make_float2(x[i], x[i + 1]), c2, mu2);
+            p.x = ex2(p.x);
+            p.y = ex2(p.y);
+            ps[e & 1] = add2(ps[e & 1], p);
             if constexpr (KV8) {                   // V row = code * scale: the scale rides on P
               const float2 k2 = reinterpret_cast<const float2*>(scale_s)[i >> 1];
-              p0 *= k2.x;
-              p1 *= k2.y;
+              p.x *= k2.x;
+              p.y *= k2.y;
             }
-            w[e] = pack_bf16(p0, p1);
+            w[e] = pack_bf16(p.x, p.y);
           }
           *reinterpret_cast<uint4*>(prow + ((u ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        l_part += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+        l_part += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
         if (j > 0 && __any_sync(0xffffffffu, move)) {   // rescale this thread's part of O
           // (at most this block's product is unfinished besides: the scores at hand were issued after all before it)
           ok = __all_sync(0xffffffffu, wait(pv_done, (at - 1) & 1, a.status, abort_flag));
@@ -639,9 +636,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
       if (ok) ok = __all_sync(0xffffffffu, wait(o_full, seg & 1, a.status, abort_flag));
       if (!ok) break;
       // row sum over both halves (fixed order: both threads get the same value)
-      put_tagged(tag_sum + tid, seg + 1, l_part);
       float l_other;
-      ok = __all_sync(0xffffffffu, get_tagged(tag_sum + (tid ^ 64), seg + 1, &l_other, a.status, abort_flag));
+      ok = exchange(l_part, &l_other);
       if (!ok) break;
       const float l_run = h == 0 ? l_part + l_other : l_other + l_part;
       // ---- epilogue: the accumulator holds columns [256 n + 128 h, + 128) of the row, n = 0, 1; staged per warp
