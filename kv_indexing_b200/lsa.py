@@ -178,7 +178,8 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return _torch().cuda.current_stream().cuda_stream
+        torch = _torch()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -550,6 +551,17 @@ def lsa_layer_group(q, w, k, seq_len, budget, layers: Sequence[dict], *, P=0, M=
 # ---------------------------------------------------------------------------
 
 
+# A decode step makes these calls for every layer and each is a few microseconds of GPU work, so the checks of
+# the binding come in two steps: _fits says in one expression whether a tensor is as it should be, and only
+# where it is not do _need, _here and _dims work out what to raise.
+
+
+def _fits(t, dtype, shape, cur):
+    """t is a dense tensor of this type and shape on device `cur`."""
+    return t is not None and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous() \
+        and t.device.index == cur
+
+
 def _here(t, name, dtype, dim):
     """_need without the demand for dense rows: strides are passed on."""
     torch = _torch()
@@ -568,10 +580,14 @@ def _here(t, name, dtype, dim):
     return t
 
 
-def _pages_of(t, name, dtype, heads, d):
+def _pages_of(t, name, dtype, heads, d, cur):
     """(page stride, row stride) in elements of a pool [n_pages, P, heads, d] or,
     for one head, [n_pages, P, d]: any page and row strides, dense rows."""
-    if t.dim() == 3 and heads == 1:
+    if t is not None and t.is_cuda and t.dtype in dtype and t.is_contiguous() and t.device.index == cur:
+        shape = t.shape
+        if len(shape) == 4 and shape[2] == heads and shape[3] == d or len(shape) == 3 and heads == 1 and shape[2] == d:
+            return shape[1] * heads * d, heads * d
+    if t is not None and t.dim() == 3 and heads == 1:
         _here(t, name, dtype, 3)
         _dims(t, name, (None, None, d))
     else:
@@ -587,15 +603,20 @@ def _pages_of(t, name, dtype, heads, d):
     return page, row
 
 
-def _table(table, seq_len, q_len, B, T):
+def _lengths(t, name, B, cur):
+    if not _fits(t, _torch().int32, (B,), cur):
+        _need(t, name, _torch().int32, 1)
+        _dims(t, name, (B,))
+
+
+def _table(table, seq_len, q_len, B, cur):
     i32 = _torch().int32
-    _need(table, "table", i32, 2)
-    _need(seq_len, "seq_len", i32, 1)
-    _dims(table, "table", (B, None))
-    _dims(seq_len, "seq_len", (B,))
+    if table is None or not _fits(table, i32, (B, table.shape[-1]), cur):
+        _need(table, "table", i32, 2)
+        _dims(table, "table", (B, None))
+    _lengths(seq_len, "seq_len", B, cur)
     if q_len is not None:
-        _need(q_len, "q_len", i32, 1)
-        _dims(q_len, "q_len", (B,))
+        _lengths(q_len, "q_len", B, cur)
 
 
 def lsa_rope_plan(rot_dim, theta, *, interleaved=False, scaling="none", factor=1.0, orig_len=0, beta_fast=32.0,
@@ -618,25 +639,25 @@ def lsa_rope(x, plan, seq_len, *, q_len=None, offset=0, inverse=False, out=None,
     transposed rotation, which takes the gradient of the output to that of x. out may be x. Returns
     out; rows of padding tokens of a given out are left as they were (a new out is zero there)."""
     torch = _torch()
-    lib = load()
-    _here(x, "x", (torch.bfloat16, torch.float32), 4)
-    _need(seq_len, "seq_len", torch.int32, 1)
-    B, T, H, d = x.shape
-    _dims(seq_len, "seq_len", (B,))
+    cur = torch.cuda.current_device()
+    if x is None or not x.is_cuda or x.device.index != cur or x.dim() != 4 or \
+            x.dtype is not torch.bfloat16 and x.dtype is not torch.float32:
+        _here(x, "x", (torch.bfloat16, torch.float32), 4)
+    B, T, H, d = shape = x.shape
+    _lengths(seq_len, "seq_len", B, cur)
     if q_len is not None:
-        _need(q_len, "q_len", torch.int32, 1)
-        _dims(q_len, "q_len", (B,))
+        _lengths(q_len, "q_len", B, cur)
     if out is None:
-        out = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
-    else:
+        out = torch.zeros(shape, dtype=x.dtype, device=x.device)
+    elif not out.is_cuda or out.device.index != cur or out.dtype is not x.dtype or out.shape != shape:
         _here(out, "out", x.dtype, 4)
-        _dims(out, "out", tuple(x.shape))
-    if d > 1 and (x.stride(3) != 1 or out.stride(3) != 1):
+        _dims(out, "out", tuple(shape))
+    xs, os = x.stride(), out.stride()
+    if d > 1 and (xs[3] != 1 or os[3] != 1):
         raise ValueError("x and out must have a dense last dimension")
-    ri = RopeIn(B, T, H, d, LSA_FP32 if x.dtype == torch.float32 else LSA_BF16, offset, int(bool(inverse)),
-                _ptr(seq_len), _ptr(q_len), _ptr(x), x.stride(0), x.stride(1), x.stride(2), out.stride(0), out.stride(1),
-                out.stride(2))
-    _check(lib.lsa_rope(ctypes.byref(ri), ctypes.byref(plan), _ptr(out), _stream(stream)))
+    ri = RopeIn(B, T, H, d, LSA_FP32 if x.dtype is torch.float32 else LSA_BF16, offset, int(bool(inverse)),
+                seq_len.data_ptr(), _ptr(q_len), x.data_ptr(), xs[0], xs[1], xs[2], os[0], os[1], os[2])
+    _check(load().lsa_rope(ri, plan, out.data_ptr(), _stream(stream)))
     return out
 
 
@@ -646,25 +667,27 @@ def lsa_pages_append(x, table, seq_len, pool, *, q_len=None, scale_pool=None, pl
     scale in scale_pool [n_pages,P] fp32. plan: every head's columns [offset, offset + rot_dim) are
     rotated first. seq_len counts the new tokens. Returns pool."""
     torch = _torch()
-    lib = load()
-    if x is not None and x.dim() == 3:
-        _need(x, "x", torch.bfloat16, 3)
-        B, T, d = x.shape
-        H = 1
-    else:
+    cur = torch.cuda.current_device()
+    if x is None or not x.is_cuda or x.dtype is not torch.bfloat16 or not x.is_contiguous() or x.device.index != cur or \
+            x.dim() not in (3, 4):
         _need(x, "x", torch.bfloat16, 4)
+    if x.dim() == 3:
+        (B, T, d), H = x.shape, 1
+    else:
         B, T, H, d = x.shape
-    _table(table, seq_len, q_len, B, T)
-    page, row = _pages_of(pool, "pool", (torch.bfloat16, torch.float8_e4m3fn), H, d)
-    e4m3 = pool.dtype == torch.float8_e4m3fn
+    _table(table, seq_len, q_len, B, cur)
+    page, row = _pages_of(pool, "pool", (torch.bfloat16, torch.float8_e4m3fn), H, d, cur)
+    n_pages, P = pool.shape[:2]
+    e4m3 = pool.dtype is torch.float8_e4m3fn
     if e4m3:
-        _need(scale_pool, "scale_pool", torch.float32, 2)
-        _dims(scale_pool, "scale_pool", tuple(pool.shape[:2]))
+        if not _fits(scale_pool, torch.float32, (n_pages, P), cur):
+            _need(scale_pool, "scale_pool", torch.float32, 2)
+            _dims(scale_pool, "scale_pool", (n_pages, P))
     elif scale_pool is not None:
         raise ValueError("scale_pool is for an e4m3 pool only")
-    ai = AppendIn(B, T, H, d, pool.shape[0], pool.shape[1], table.shape[1], LSA_E4M3 if e4m3 else LSA_BF16, offset,
-                  _ptr(seq_len), _ptr(q_len), _ptr(table), _ptr(x), _ptr(pool), page, row, _ptr(scale_pool))
-    _check(lib.lsa_pages_append(ctypes.byref(ai), ctypes.byref(plan) if plan is not None else None, _stream(stream)))
+    ai = AppendIn(B, T, H, d, n_pages, P, table.shape[1], LSA_E4M3 if e4m3 else LSA_BF16, offset, seq_len.data_ptr(),
+                  _ptr(q_len), table.data_ptr(), x.data_ptr(), pool.data_ptr(), page, row, _ptr(scale_pool))
+    _check(load().lsa_pages_append(ai, plan, _stream(stream)))
     return pool
 
 
@@ -673,32 +696,40 @@ def paged_attn_in(q, table, seq_len, scale, *, kv=None, k=None, v=None, d_v=None
     """Describe paged attention: q [B,T,Hq,d_qk] bf16; latent rows kv [n_pages,P,576] (bf16, or
     torch.float8_e4m3fn with kv_scale [n_pages,P]), or k, v [n_pages,P,Hkv,d] bf16."""
     torch = _torch()
-    _need(q, "q", torch.bfloat16, 4)
+    cur = torch.cuda.current_device()
+    if q is None or q.dim() != 4 or not _fits(q, torch.bfloat16, q.shape, cur):
+        _need(q, "q", torch.bfloat16, 4)
     B, T, Hq, d_qk = q.shape
-    _table(table, seq_len, q_len, B, T)
+    _table(table, seq_len, q_len, B, cur)
     if kv is not None:
         if k is not None or v is not None:
             raise ValueError("give kv (latent rows) or k and v, not both")
-        page, row = _pages_of(kv, "kv", (torch.bfloat16, torch.float8_e4m3fn), 1, d_qk)
-        e4m3 = kv.dtype == torch.float8_e4m3fn
+        page, row = _pages_of(kv, "kv", (torch.bfloat16, torch.float8_e4m3fn), 1, d_qk, cur)
+        n_pages, P = kv.shape[:2]
+        e4m3 = kv.dtype is torch.float8_e4m3fn
         if e4m3:
-            _need(kv_scale, "kv_scale", torch.float32, 2)
-            _dims(kv_scale, "kv_scale", tuple(kv.shape[:2]))
+            if not _fits(kv_scale, torch.float32, (n_pages, P), cur):
+                _need(kv_scale, "kv_scale", torch.float32, 2)
+                _dims(kv_scale, "kv_scale", (n_pages, P))
         elif kv_scale is not None:
             raise ValueError("kv_scale is for an e4m3 kv only")
-        return PagedAttnIn(B, T, Hq, 1, d_qk, d_v if d_v is not None else 512, kv.shape[0], kv.shape[1], table.shape[1],
-                           float(scale), LSA_E4M3 if e4m3 else LSA_BF16, _ptr(seq_len), _ptr(q_len), _ptr(table), _ptr(q),
-                           _ptr(kv), _ptr(kv), page, row, page, row, _ptr(kv_scale))
+        at = kv.data_ptr()
+        return PagedAttnIn(B, T, Hq, 1, d_qk, d_v if d_v is not None else 512, n_pages, P, table.shape[1], scale,
+                           LSA_E4M3 if e4m3 else LSA_BF16, seq_len.data_ptr(), _ptr(q_len), table.data_ptr(), q.data_ptr(),
+                           at, at, page, row, page, row, _ptr(kv_scale))
     if kv_scale is not None:
         raise ValueError("kv_scale is for an e4m3 kv only")
-    _here(k, "k", torch.bfloat16, 4)
-    Hkv = k.shape[2]
-    kp, kr = _pages_of(k, "k", torch.bfloat16, Hkv, d_qk)
-    _here(v, "v", torch.bfloat16, 4)
-    vp, vr = _pages_of(v, "v", torch.bfloat16, Hkv, v.shape[3])
-    _dims(v, "v", (k.shape[0], k.shape[1], Hkv, d_v))
-    return PagedAttnIn(B, T, Hq, Hkv, d_qk, v.shape[3], k.shape[0], k.shape[1], table.shape[1], float(scale), LSA_BF16,
-                       _ptr(seq_len), _ptr(q_len), _ptr(table), _ptr(q), _ptr(k), _ptr(v), kp, kr, vp, vr, None)
+    if k is None or v is None or k.dim() != 4 or v.dim() != 4:
+        _here(k, "k", torch.bfloat16, 4)
+        _here(v, "v", torch.bfloat16, 4)
+    n_pages, P, Hkv = k.shape[:3]
+    kp, kr = _pages_of(k, "k", (torch.bfloat16,), Hkv, d_qk, cur)
+    vd = v.shape[3]
+    vp, vr = _pages_of(v, "v", (torch.bfloat16,), Hkv, vd, cur)
+    if v.shape != (n_pages, P, Hkv, vd if d_v is None else d_v):
+        _dims(v, "v", (n_pages, P, Hkv, d_v))
+    return PagedAttnIn(B, T, Hq, Hkv, d_qk, vd, n_pages, P, table.shape[1], scale, LSA_BF16, seq_len.data_ptr(), _ptr(q_len),
+                       table.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), kp, kr, vp, vr, None)
 
 
 def lsa_paged_attn(q, table, seq_len, scale, *, kv=None, k=None, v=None, d_v=None, kv_scale=None, q_len=None, out=None,
@@ -710,91 +741,98 @@ def lsa_paged_attn(q, table, seq_len, scale, *, kv=None, k=None, v=None, d_v=Non
     torch = _torch()
     lib = load()
     pi = paged_attn_in(q, table, seq_len, scale, kv=kv, k=k, v=v, d_v=d_v, kv_scale=kv_scale, q_len=q_len)
-    shape = (pi.B, pi.T, pi.Hq, pi.d_v)
+    shape, cur = (pi.B, pi.T, pi.Hq, pi.d_v), q.device.index
     if out is None:
-        make = torch.empty if q_len is None else torch.zeros
-        out = make(shape, dtype=torch.bfloat16, device=q.device)
-    _out(out, "out", torch.bfloat16, shape)
-    _out(lse, "lse", torch.float32, shape[:3])
-    ws = _workspace(workspace_size(LSA_OP_PAGED_ATTN, paged=pi), q.device, workspace)
-    _check(lib.lsa_paged_attn(ctypes.byref(pi), _ptr(out), _ptr(lse), _ptr(ws), _nbytes(ws), _stream(stream)))
+        out = (torch.empty if q_len is None else torch.zeros)(shape, dtype=torch.bfloat16, device=q.device)
+    elif not _fits(out, torch.bfloat16, shape, cur):
+        _out(out, "out", torch.bfloat16, shape)
+    if lse is not None and not _fits(lse, torch.float32, shape[:3], cur):
+        _out(lse, "lse", torch.float32, shape[:3])
+    args, size = OpArgs(paged=ctypes.pointer(pi)), ctypes.c_size_t()
+    _check(lib.lsa_workspace_size(LSA_OP_PAGED_ATTN, args, size))
+    ws = _workspace(size.value, q.device, workspace)
+    _check(lib.lsa_paged_attn(pi, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.nbytes, _stream(stream)))
     return out, lse
 
 
 def _cache(table, ref, seq_len=None):
-    """(S, max_pages, n_pages) of a table [S,max_pages] and counts ref [n_pages], all int32."""
-    i32 = _torch().int32
-    _need(table, "table", i32, 2)
-    _need(ref, "ref", i32, 1)
+    """(S, max_pages, n_pages, device) of a table [S,max_pages] and counts ref [n_pages], all int32."""
+    i32, cur = _torch().int32, _torch().cuda.current_device()
+    if table is None or table.dim() != 2 or not _fits(table, i32, table.shape, cur):
+        _need(table, "table", i32, 2)
+    if ref is None or ref.dim() != 1 or not _fits(ref, i32, ref.shape, cur):
+        _need(ref, "ref", i32, 1)
+    S, max_pages = table.shape
     if seq_len is not None:
-        _need(seq_len, "seq_len", i32, 1)
-        _dims(seq_len, "seq_len", (table.shape[0],))
-    return table.shape[0], table.shape[1], ref.shape[0]
+        _lengths(seq_len, "seq_len", S, cur)
+    return S, max_pages, ref.shape[0], cur
 
 
-def _list(t, name, n=None):
-    i32 = _torch().int32
-    _need(t, name, i32, 1)
-    if n is not None:
-        _dims(t, name, (n,))
+def _list(t, name, cur):
+    if t is None or t.dim() != 1 or not _fits(t, _torch().int32, t.shape, cur):
+        _need(t, name, _torch().int32, 1)
     return t.shape[0]
 
 
-def _pools(pools, n_pages):
+def _pools(pools, n_pages, cur):
     """Descriptors of pools [n_pages, ...]: any page stride, dense pages of a multiple of 16 bytes."""
-    cur = _torch().cuda.current_device()
-    arr = (Pool * max(1, len(pools)))()
+    rows = []
     for i, t in enumerate(pools):
         if not t.is_cuda or t.device.index != cur:
             raise ValueError(f"pools[{i}] must be a CUDA tensor on the current device cuda:{cur}")
-        if t.dim() < 2 or t.shape[0] != n_pages:
-            raise ValueError(f"pools[{i}] has shape {tuple(t.shape)}, expected ({n_pages}, ...)")
-        if not t[0].is_contiguous():
-            raise ValueError(f"pools[{i}]: a page must be contiguous")
+        shape = t.shape
+        if len(shape) < 2 or shape[0] != n_pages:
+            raise ValueError(f"pools[{i}] has shape {tuple(shape)}, expected ({n_pages}, ...)")
+        strides, page = t.stride(), 1
+        for n, step in zip(shape[:0:-1], strides[:0:-1]):
+            if step != page and n != 1:
+                raise ValueError(f"pools[{i}]: a page must be contiguous")
+            page *= n
         es = t.element_size()
-        page = t[0].numel() * es
-        arr[i] = Pool(t.data_ptr(), page, t.stride(0) * es if n_pages > 1 else page)
-    return arr
+        rows.append((t.data_ptr(), page * es, (strides[0] if n_pages > 1 else page) * es))
+    return (Pool * max(1, len(rows)))(*rows)
 
 
 def lsa_pages_reserve(table, ref, lens, page_size, *, stream=None):
     """Maps pages (the lowest free ones) until row s of table [S,max_pages] holds lens[s] tokens."""
-    S, max_pages, n_pages = _cache(table, ref)
-    _list(lens, "lens", S)
-    _check(load().lsa_pages_reserve(_ptr(table), _ptr(ref), _ptr(lens), S, max_pages, n_pages, page_size,
+    S, max_pages, n_pages, cur = _cache(table, ref)
+    _lengths(lens, "lens", S, cur)
+    _check(load().lsa_pages_reserve(table.data_ptr(), ref.data_ptr(), lens.data_ptr(), S, max_pages, n_pages, page_size,
                                     _stream(stream)))
 
 
 def lsa_pages_free(table, ref, seq_len, seqs, *, stream=None):
     """Frees the sequences seqs [n]: their pages' counts - 1, rows unmapped, lengths 0."""
-    S, max_pages, n_pages = _cache(table, ref, seq_len)
-    n = _list(seqs, "seqs")
-    _check(load().lsa_pages_free(_ptr(table), _ptr(ref), _ptr(seq_len), S, max_pages, n_pages, _ptr(seqs), n,
-                                 _stream(stream)))
+    S, max_pages, n_pages, cur = _cache(table, ref, seq_len)
+    n = _list(seqs, "seqs", cur)
+    _check(load().lsa_pages_free(table.data_ptr(), ref.data_ptr(), seq_len.data_ptr(), S, max_pages, n_pages,
+                                 seqs.data_ptr(), n, _stream(stream)))
 
 
 def lsa_pages_fork(table, ref, seq_len, page_size, parent, child, pools: Sequence, *, workspace=None, stream=None):
     """Makes sequences child[i] copies of parent[i]: full pages shared, a partly filled last page
     copied in every pool. Children must be free (lsa_pages_free)."""
-    S, max_pages, n_pages = _cache(table, ref, seq_len)
-    n = _list(parent, "parent")
-    _list(child, "child", n)
-    arr = _pools(pools, n_pages)
-    ws = _workspace(workspace_size(LSA_OP_PAGES_FORK, n=n), table.device, workspace)
-    _check(load().lsa_pages_fork(_ptr(table), _ptr(ref), _ptr(seq_len), S, max_pages, n_pages, page_size, _ptr(parent),
-                                 _ptr(child), n, arr, len(pools), _ptr(ws), _nbytes(ws), _stream(stream)))
+    S, max_pages, n_pages, cur = _cache(table, ref, seq_len)
+    n = _list(parent, "parent", cur)
+    _lengths(child, "child", n, cur)
+    arr = _pools(pools, n_pages, cur)
+    ws = _workspace(_pages_bytes(LSA_OP_PAGES_FORK, n, 0), table.device, workspace)
+    _check(load().lsa_pages_fork(table.data_ptr(), ref.data_ptr(), seq_len.data_ptr(), S, max_pages, n_pages, page_size,
+                                 parent.data_ptr(), child.data_ptr(), n, arr, len(pools), _ptr(ws), _nbytes(ws),
+                                 _stream(stream)))
 
 
 def lsa_pages_copy(pools: Sequence, src, dst, *, workspace=None, stream=None):
     """Copies page src[i] to dst[i] in every pool [n_pages, ...]."""
     if not len(pools):
         raise ValueError("need at least one pool")
+    cur = _torch().cuda.current_device()
     n_pages = pools[0].shape[0]
-    n = _list(src, "src")
-    _list(dst, "dst", n)
-    arr = _pools(pools, n_pages)
-    ws = _workspace(workspace_size(LSA_OP_PAGES_COPY, n=n), src.device, workspace)
-    _check(load().lsa_pages_copy(arr, len(pools), n_pages, _ptr(src), _ptr(dst), n, _ptr(ws), _nbytes(ws),
+    n = _list(src, "src", cur)
+    _lengths(dst, "dst", n, cur)
+    arr = _pools(pools, n_pages, cur)
+    ws = _workspace(_pages_bytes(LSA_OP_PAGES_COPY, n, 0), src.device, workspace)
+    _check(load().lsa_pages_copy(arr, len(pools), n_pages, src.data_ptr(), dst.data_ptr(), n, _ptr(ws), _nbytes(ws),
                                  _stream(stream)))
 
 
@@ -803,17 +841,31 @@ def lsa_pages_compact(table, ref, pools: Sequence, *, table_out=None, ref_out=No
     """Packs the live pages into the first n_live pages of every pool. table_out and ref_out default to
     table and ref themselves. Returns (table_out, ref_out, n_live [1] int32)."""
     torch = _torch()
-    S, max_pages, n_pages = _cache(table, ref)
-    table_out = table if table_out is None else _out(table_out, "table_out", torch.int32, (S, max_pages))
-    ref_out = ref if ref_out is None else _out(ref_out, "ref_out", torch.int32, (n_pages,))
+    S, max_pages, n_pages, cur = _cache(table, ref)
+    if table_out is None:
+        table_out = table
+    elif not _fits(table_out, torch.int32, (S, max_pages), cur):
+        _out(table_out, "table_out", torch.int32, (S, max_pages))
+    if ref_out is None:
+        ref_out = ref
+    elif not _fits(ref_out, torch.int32, (n_pages,), cur):
+        _out(ref_out, "ref_out", torch.int32, (n_pages,))
     if n_live is None:
         n_live = torch.empty(1, dtype=torch.int32, device=table.device)
-    _out(n_live, "n_live", torch.int32, (1,))
-    arr = _pools(pools, n_pages)
-    ws = _workspace(workspace_size(LSA_OP_PAGES_COMPACT, n_pages=n_pages), table.device, workspace)
-    _check(load().lsa_pages_compact(_ptr(table), _ptr(ref), S, max_pages, n_pages, arr, len(pools), _ptr(table_out),
-                                    _ptr(ref_out), _ptr(n_live), _ptr(ws), _nbytes(ws), _stream(stream)))
+    elif not _fits(n_live, torch.int32, (1,), cur):
+        _out(n_live, "n_live", torch.int32, (1,))
+    arr = _pools(pools, n_pages, cur)
+    ws = _workspace(_pages_bytes(LSA_OP_PAGES_COMPACT, 0, n_pages), table.device, workspace)
+    _check(load().lsa_pages_compact(table.data_ptr(), ref.data_ptr(), S, max_pages, n_pages, arr, len(pools),
+                                    table_out.data_ptr(), ref_out.data_ptr(), n_live.data_ptr(), _ptr(ws), _nbytes(ws),
+                                    _stream(stream)))
     return table_out, ref_out, n_live
+
+
+def _pages_bytes(op, n, n_pages):
+    size = ctypes.c_size_t()
+    _check(load().lsa_workspace_size(op, OpArgs(n=n, n_pages=n_pages), size))
+    return size.value
 
 
 def lsa_device_status(stream=None) -> int:

@@ -201,6 +201,7 @@ class _Strided(_DeviceTensor):
             s.insert(0, n)
             n *= m
         self._strides = strides or tuple(s)
+        self._contiguous = self._strides == tuple(s)
 
     def stride(self, i=None):
         return self._strides if i is None else self._strides[i]
