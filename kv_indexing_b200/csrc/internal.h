@@ -206,7 +206,7 @@ struct RotateArgs {
   float* scales;          // e4m3 pool: per-token scales [n_pages, page_size]
   int vec;                // elements per access: 16 bytes, or 1
   int* status;
-  double freq[LSA_ROPE_MAX_PAIRS];
+  double freq[LSA_ROPE_MAX_PAIRS];   // turns per position of pair i
 };
 cudaError_t launch_rope(const RotateArgs& a, int fp32, cudaStream_t stream);
 cudaError_t launch_append(const RotateArgs& a, int e4m3, cudaStream_t stream);

@@ -5,7 +5,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstring>
 #include <mutex>
 
 #include "internal.h"
@@ -51,7 +50,7 @@ void put_plan(RotateArgs* a, const lsa_rope_plan_t* p) {
   a->rot = p->rot_dim;
   a->interleaved = p->interleaved != 0;
   a->amplitude = static_cast<float>(p->amplitude);
-  std::memcpy(a->freq, p->freq, sizeof(a->freq));
+  for (int i = 0; i < LSA_ROPE_MAX_PAIRS; ++i) a->freq[i] = p->freq[i] / 6.283185307179586477;   // turns per position
 }
 
 // ------------------------------------------------------------ tensor maps --

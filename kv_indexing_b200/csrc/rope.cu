@@ -3,10 +3,10 @@
 //   a = pos * f_i,  y0 = m (x0 cos a - s x1 sin a),  y1 = m (x1 cos a + s x0 sin a)
 //
 // for pair i of a row at position pos (s = -1: the transposed rotation, which
-// is the gradient). The angle is a 64-bit product reduced to [-pi, pi] in 64
-// bits: at position 10^6 a 32-bit product alone is off by 0.06 rad. Sine and
-// cosine are those of the angle's fp32 head, with its tail added to first
-// order; they and the rotation are fp32. A result is rounded once.
+// is the gradient). The angle, in turns, is a 64-bit product whose whole turns
+// are dropped in 64 bits: at position 10^6 a 32-bit product alone is off by 0.06
+// rad. Sine and cosine are those of the angle's fp32 head, with its tail added to
+// first order; they and the rotation are fp32. A result is rounded once.
 //
 // Bound by bytes: every row is read and written once. A block takes a few
 // tokens, computes their angles once into shared memory (they are the same for
@@ -14,6 +14,8 @@
 // over rows, four rows in flight.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -53,14 +55,14 @@ __device__ __forceinline__ int token_pos(const RotateArgs& a, int b, int t) {
   return pos < 0 ? -1 : static_cast<int>(pos);
 }
 
-// m cos a, s m sin a of pair i at position pos.
+// m cos a, s m sin a of pair i at position pos. a.freq is in turns: the turns of
+// pos are reduced to [-1/2, 1/2] by a subtraction that is exact.
 __device__ __forceinline__ float2 turn_of(const RotateArgs& a, int pos, int i) {
   const double w = static_cast<double>(pos) * a.freq[i];
-  const double k = rint(w * 0.15915494309189533577);            // 1 / (2 pi)
-  const double r = fma(-k, 2.4492935982947064e-16, fma(-k, 6.283185307179586477, w));   // 2 pi in two doubles
-  const float hi = static_cast<float>(r), lo = static_cast<float>(r - hi);
+  const double r = 2.0 * (w - rint(w));                          // half turns
+  const float hi = static_cast<float>(r), lo = static_cast<float>(r - hi) * 3.14159265358979f;
   float s, c;
-  sincosf(hi, &s, &c);
+  sincospif(hi, &s, &c);
   return make_float2(a.amplitude * fmaf(-lo, s, c), a.sign * a.amplitude * fmaf(lo, c, s));   // to first order in lo
 }
 
@@ -92,6 +94,51 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
   const int h0 = blockIdx.y * heads_per_block;
   const int nh = min(heads_per_block, a.H - h0);
   const int pairs = a.rot / 2;
+  constexpr int kUnitPairs = INTER ? (VEC > 1 ? VEC / 2 : 1) : VEC;
+  constexpr int kPacks = (INTER && VEC > 1) ? 1 : 2;             // packs of a rotated unit
+  const int n_rot = pairs / kUnitPairs;
+  const int n_copy = a.in_place ? 0 : (a.d - a.rot) / VEC;
+  const int units = n_rot + n_copy;
+  const int rows = n_tok * nh;
+  using P = Pack<T, VEC>;
+  const T* x = static_cast<const T*>(a.x);
+  T* out = static_cast<T*>(a.out);
+  P v0[kInFlight], v1[kInFlight];
+  // The unit's columns, and the rows that this thread has of it: r0, r0 + r_step, ...
+  bool rotated;
+  int u, r0, r_step, c0, c1;
+  auto unit_of = [&](int u0) {
+    const int nu = min(kThreads, units - u0);
+    r_step = kThreads / nu;
+    u = u0 + threadIdx.x % nu;
+    r0 = threadIdx.x / nu;
+    if (r0 >= r_step) r0 = rows;                  // threads left over
+    rotated = u < n_rot;
+    if (rotated) {
+      c0 = a.offset + (INTER ? u * 2 * kUnitPairs : u * VEC);
+      c1 = c0 + (INTER ? 1 : pairs);              // INTER with VEC = 1: the odd column
+    } else {
+      c0 = (u - n_rot) * VEC;
+      if (c0 >= a.offset) c0 += a.rot;
+      c1 = c0;
+    }
+  };
+  auto load = [&](int r) {
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k) {
+      const int rr = r + k * r_step;
+      if (rr < rows) {
+        const int tok = rr / nh, h = h0 + rr - tok * nh;
+        const int b = (n0 + tok) / a.T, t = (n0 + tok) - b * a.T;
+        const T* src = x + b * a.xb + t * a.xt + h * a.xh;
+        v0[k] = *reinterpret_cast<const P*>(src + c0);
+        if (kPacks == 2 && rotated) v1[k] = *reinterpret_cast<const P*>(src + c1);
+      }
+    }
+  };
+  // the first rows are on their way while the angles are computed
+  unit_of(0);
+  load(r0);
   for (int i = threadIdx.x; i < n_tok; i += kThreads) {
     const int b = (n0 + i) / a.T, t = (n0 + i) - b * a.T;
     const int pos = token_pos(a, b, t);
@@ -113,57 +160,21 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
     cs[i] = pos >= 0 ? turn_of(a, pos, p) : make_float2(1.f, 0.f);
   }
   __syncthreads();
-  constexpr int kUnitPairs = INTER ? (VEC > 1 ? VEC / 2 : 1) : VEC;
-  constexpr int kPacks = (INTER && VEC > 1) ? 1 : 2;             // packs of a rotated unit
-  const int n_rot = pairs / kUnitPairs;
-  const int n_copy = a.in_place ? 0 : (a.d - a.rot) / VEC;
-  const int units = n_rot + n_copy;
-  const int rows = n_tok * nh;
-  using P = Pack<T, VEC>;
-  const T* x = static_cast<const T*>(a.x);
-  T* out = static_cast<T*>(a.out);
   // units per pass of the block: all of them, or kThreads at a time
   for (int u0 = 0; u0 < units; u0 += kThreads) {
-    const int nu = min(kThreads, units - u0);
-    const int r_step = kThreads / nu;
-    const int u = u0 + threadIdx.x % nu;
-    const int r0 = threadIdx.x / nu;
-    if (r0 >= r_step) continue;
-    const bool rotated = u < n_rot;
-    int c0, c1;                                   // columns of the unit's packs
-    if (rotated) {
-      c0 = a.offset + (INTER ? u * 2 * kUnitPairs : u * VEC);
-      c1 = c0 + (INTER ? 1 : pairs);              // INTER with VEC = 1: the odd column
-    } else {
-      c0 = (u - n_rot) * VEC;
-      if (c0 >= a.offset) c0 += a.rot;
-      c1 = c0;
-    }
+    if (u0) unit_of(u0);
     for (int r = r0; r < rows; r += r_step * kInFlight) {
-      P v0[kInFlight], v1[kInFlight];
-      long long o[kInFlight];
-      int tk[kInFlight];
+      if (u0 || r != r0) load(r);
 #pragma unroll
       for (int k = 0; k < kInFlight; ++k) {
         const int rr = r + k * r_step;
-        o[k] = -1;
-        if (rr < rows) {
-          const int tok = rr / nh, h = h0 + rr - tok * nh;
-          tk[k] = tok;
-          if (s_out[tok] >= 0) {
-            o[k] = s_out[tok] + h * a.oh;
-            const int b = (n0 + tok) / a.T, t = (n0 + tok) - b * a.T;
-            const T* src = x + b * a.xb + t * a.xt + h * a.xh;
-            v0[k] = *reinterpret_cast<const P*>(src + c0);
-            if (kPacks == 2 && rotated) v1[k] = *reinterpret_cast<const P*>(src + c1);
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kInFlight; ++k) {
-        if (o[k] < 0) continue;
+        if (rr >= rows) continue;
+        const int tok = rr / nh, h = h0 + rr - tok * nh;
+        const long long to = s_out[tok];
+        if (to < 0) continue;
+        T* dst = out + to + h * a.oh;
         if (rotated) {
-          const float2* t = cs + tk[k] * pairs + u * kUnitPairs;
+          const float2* t = cs + tok * pairs + u * kUnitPairs;
           if (kPacks == 1) {
 #pragma unroll
             for (int e = 0; e < VEC / 2; ++e) {
@@ -180,51 +191,59 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
               v0[k].v[e] = from_f<T>(x0 * w.x - x1 * w.y);
               v1[k].v[e] = from_f<T>(x1 * w.x + x0 * w.y);
             }
-            *reinterpret_cast<P*>(out + o[k] + c1) = v1[k];
+            *reinterpret_cast<P*>(dst + c1) = v1[k];
           }
         }
-        *reinterpret_cast<P*>(out + o[k] + c0) = v0[k];
+        *reinterpret_cast<P*>(dst + c0) = v0[k];
       }
     }
   }
 }
 
-// New rows -> e4m3 codes with a per-token scale. One warp per token; the row
-// (<= 1024 columns, 8 per lane and pass) stays in registers between its
-// maximum and its codes. Divisions are IEEE divisions: the codes are those of
+// New rows -> e4m3 codes with a per-token scale. Half a warp per token: the row
+// (<= 1024 columns, 8 per lane and pass) stays in registers between its maximum
+// and its codes. Quotients are rounded as divisions are: the codes are those of
 // the formula, not of a product with a reciprocal.
-constexpr int kRowPasses = 4;
+constexpr int kRowLanes = 16, kRowPasses = 8;
+constexpr int kRowsPerBlock = kThreads / kRowLanes;
 template <bool INTER>
 __global__ void __launch_bounds__(kThreads) append_e4m3_kernel(const __grid_constant__ RotateArgs a) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ float2 cs_all[];             // [warps][rot / 2]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = blockIdx.x * (kThreads / 32) + warp;
-  if (n >= a.B * a.T) return;
-  const int b = n / a.T, t = n - b * a.T;
-  const int pos = token_pos(a, b, t);
-  if (pos < 0) return;
-  const int2 sl = slot_of(a, b, pos);
-  if (sl.x < 0) return;
+  extern __shared__ float2 cs_all[];             // [rows of the block][rot / 2]
+  const int lane = threadIdx.x % kRowLanes, in_block = threadIdx.x / kRowLanes;
+  const int n = blockIdx.x * kRowsPerBlock + in_block;
+  const bool exists = n < a.B * a.T;
+  const int b = exists ? n / a.T : 0, t = exists ? n - b * a.T : 0;
   const int pairs = a.rot / 2;
-  float2* cs = cs_all + warp * pairs;
-  for (int i = lane; i < pairs; i += 32) cs[i] = turn_of(a, pos, i);
-  __syncwarp();
-  const int vecs = a.H * a.d / 8;
+  float2* cs = cs_all + in_block * pairs;
+  const int vecs = exists ? a.H * a.d / 8 : 0;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.x) + static_cast<long long>(n) * a.H * a.d;
   using P = Pack<__nv_bfloat16, 8>;
+  P raw[kRowPasses];
+#pragma unroll
+  for (int q = 0; q < kRowPasses; ++q) {         // on their way while position, page and angles are worked out
+    const int u = q * kRowLanes + lane;
+    if (u < vecs) raw[q] = *reinterpret_cast<const P*>(src + u * 8);
+  }
+  const int pos = exists ? token_pos(a, b, t) : -1;
+  int2 sl = make_int2(-1, 0);
+  if (pos >= 0) {
+    sl = slot_of(a, b, pos);
+    for (int i = lane; i < pairs; i += kRowLanes) cs[i] = turn_of(a, pos, i);
+  }
+  __syncwarp();
   float v[kRowPasses][8];
   float amax = 0.f;
 #pragma unroll
   for (int q = 0; q < kRowPasses; ++q) {
-    const int u = q * 32 + lane;
+    const int u = q * kRowLanes + lane;
     if (u >= vecs) continue;
-    const P p = *reinterpret_cast<const P*>(src + u * 8);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[q][e] = __bfloat162float(p.v[e]);
-    const int h = u * 8 / a.d, c = u * 8 - h * a.d - a.offset;   // column within the rotated part
-    if (c >= 0 && c < a.rot) {
+    for (int e = 0; e < 8; ++e) v[q][e] = __bfloat162float(raw[q].v[e]);
+    const int h = a.H > 1 ? u * 8 / a.d : 0;
+    const int c = u * 8 - h * a.d - a.offset;    // column within the rotated part
+    if (pos >= 0 && c >= 0 && c < a.rot) {
       if (INTER) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -235,11 +254,11 @@ __global__ void __launch_bounds__(kThreads) append_e4m3_kernel(const __grid_cons
         }
       } else {   // the other half of the pair comes from its own columns
         const bool low = c < pairs;
-        const P o = *reinterpret_cast<const P*>(src + u * 8 + (low ? pairs : -pairs));
+        const P other = *reinterpret_cast<const P*>(src + u * 8 + (low ? pairs : -pairs));
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float2 w = cs[(low ? c : c - pairs) + e];
-          const float y = __bfloat162float(o.v[e]);
+          const float y = __bfloat162float(other.v[e]);
           v[q][e] = low ? v[q][e] * w.x - y * w.y : v[q][e] * w.x + y * w.y;
         }
       }
@@ -248,19 +267,34 @@ __global__ void __launch_bounds__(kThreads) append_e4m3_kernel(const __grid_cons
     for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(v[q][e]));
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int o = kRowLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (sl.x < 0) return;
   const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+  // x / scale by one division for the row: with 1 / scale rounded correctly, a product and one residual step round
+  // the quotient correctly (Markstein 1990), away from the ends of the exponent range. A division for every column
+  // bounds the kernel by instructions.
+  const bool divide = !(scale > 1e-30f && scale < 1e30f);
+  const float inv = __frcp_rn(scale);
   uint8_t* dst = static_cast<uint8_t*>(a.out) + sl.x * a.ob + sl.y * a.ot;
 #pragma unroll
   for (int q = 0; q < kRowPasses; ++q) {
-    const int u = q * 32 + lane;
+    const int u = q * kRowLanes + lane;
     if (u >= vecs) continue;
-    uint32_t w[2] = {0u, 0u};
+    if (divide) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      w[e >> 2] |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(__fdiv_rn(v[q][e], scale), __NV_SATFINITE, __NV_E4M3))
-                   << (8 * (e & 3));
-    *reinterpret_cast<uint2*>(dst + u * 8) = make_uint2(w[0], w[1]);
+      for (int e = 0; e < 8; ++e) v[q][e] = __fdiv_rn(v[q][e], scale);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = v[q][e] * inv;
+        v[q][e] = fmaf(fmaf(-x, scale, v[q][e]), inv, x);
+      }
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = __nv_cvt_float2_to_fp8x2(make_float2(v[q][2 * e], v[q][2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
+    *reinterpret_cast<uint2*>(dst + u * 8) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
   }
   if (lane == 0) a.scales[static_cast<long long>(sl.x) * a.page_size + sl.y] = scale;
 }
@@ -269,22 +303,17 @@ template <class T, int VEC, bool PAGED>
 cudaError_t launch_t(const RotateArgs& a, cudaStream_t stream) {
   const void* fn = a.interleaved ? reinterpret_cast<const void*>(&rotate_kernel<T, VEC, true, PAGED>)
                                  : reinterpret_cast<const void*>(&rotate_kernel<T, VEC, false, PAGED>);
-  // A block's share: about kInFlight packs per thread (32 KB for 16-byte packs),
-  // in whole tokens, or part of the heads of one token when its rows alone are more.
+  // A block's share: about kInFlight packs per thread (32 KB for 16-byte packs), fewer where that leaves SMs without
+  // a block; in whole tokens, or part of the heads of one token when its rows alone are more.
   const long long n = static_cast<long long>(a.B) * a.T;
   const int units = a.in_place ? a.rot / VEC : a.d / VEC;
-  const long long per_tok = static_cast<long long>(units > 0 ? units : 1) * a.H;
-  const long long target = static_cast<long long>(kThreads) * kInFlight;
-  long long tok = target / per_tok;
-  if (tok < 1) tok = 1;
-  if (tok > kMaxTok) tok = kMaxTok;
-  // few tokens: spread them over the GPU
-  const long long even = (n + device_sm_count() - 1) / device_sm_count();
-  if (tok > even) tok = even;
+  const long long per_row = units > 0 ? units : 1, per_tok = per_row * a.H;
+  const long long even = (n * per_tok + device_sm_count() - 1) / device_sm_count();
+  const long long target = std::max(std::min(even, static_cast<long long>(kThreads) * kInFlight), static_cast<long long>(kThreads));
+  const long long tok = std::max(1ll, std::min(target / per_tok, static_cast<long long>(kMaxTok)));
   int heads = a.H;
-  if (tok == 1 && per_tok > target) {
-    heads = static_cast<int>((target + units - 1) / units);
-    if (n * ((a.H + heads - 1) / heads) < device_sm_count()) heads = (heads + 3) / 4;
+  if (per_tok > target) {
+    heads = static_cast<int>((target + per_row - 1) / per_row);
     if ((a.H + heads - 1) / heads > 65535) heads = (a.H + 65534) / 65535;
   }
   const dim3 grid(static_cast<unsigned>((n + tok - 1) / tok), (a.H + heads - 1) / heads);
@@ -304,7 +333,7 @@ cudaError_t launch_rope(const RotateArgs& a, int fp32, cudaStream_t stream) {
 cudaError_t launch_append(const RotateArgs& a, int e4m3, cudaStream_t stream) {
   if (!e4m3) return launch_t<__nv_bfloat16, 8, true>(a, stream);
   const long long n = static_cast<long long>(a.B) * a.T;
-  const int per = kThreads / 32;
+  const int per = kRowsPerBlock;
   const void* fn = a.interleaved ? reinterpret_cast<const void*>(&append_e4m3_kernel<true>)
                                  : reinterpret_cast<const void*>(&append_e4m3_kernel<false>);
   void* args[] = {const_cast<RotateArgs*>(&a)};
