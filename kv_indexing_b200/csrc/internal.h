@@ -264,12 +264,10 @@ struct PagedArgs {
   float* part_o;          // [2 * workers][tile_rows][d_v], each normalised by its own sum
   float* part_m;          // [2 * workers][tile_rows], log2 domain
   float* part_l;
-  const uint8_t* kv8;     // e4m3 latent rows (else null)
-  long long kv8_page, kv8_row;
-  const float* k_scale;   // [n_pages, page_size]
+  const float* k_scale;   // e4m3: [n_pages, page_size]
   int* status;
 };
-// K and V as (columns, slot, page) with boxes of 64 columns x box rows x 1 page.
+// K and V as (columns, slot, page) with boxes of 64 columns (e4m3: 128) x box rows x 1 page.
 struct PagedMaps {
   CUtensorMap k, v;
 };
@@ -277,7 +275,7 @@ constexpr int kPagedBN = 128;      // keys per block
 constexpr int kPagedBox = 64;      // most rows of a box, latent rows
 constexpr int kMaxWorkers = 160;   // a merge keeps one weight per worker
 cudaError_t launch_paged_attn(const PagedMaps& m, const PagedArgs& a, int d, int shared_kv, cudaStream_t stream);
-cudaError_t launch_paged_mla(const PagedMaps& m, const PagedArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_mla(const PagedMaps& m, const PagedArgs& a, int e4m3, cudaStream_t stream);
 cudaError_t launch_paged_combine(const PagedArgs& a, int d_v, cudaStream_t stream);
 
 lsa_status_t paged_attn_workspace(const lsa_paged_attn_in_t* in, size_t* bytes);

@@ -67,18 +67,21 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// bf16 pages as (columns, slot, page), boxes of 64 columns x box_rows x 1.
-lsa_status_t page_map(CUtensorMap* m, const void* base, int cols, int page_size, int n_pages, int64_t row_stride,
+// Pages as (columns, slot, page). bf16: boxes of 64 columns x box_rows x 1, swizzled as the MMA reads them; e4m3 codes:
+// boxes of 128 columns, plain.
+lsa_status_t page_map(CUtensorMap* m, const void* base, bool e4m3, int cols, int page_size, int n_pages, int64_t row_stride,
                       int64_t page_stride, int box_rows) {
   auto fn = encoder();
   if (!fn) return set_error(LSA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const int es = e4m3 ? 1 : 2;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(page_size),
                         static_cast<cuuint64_t>(n_pages)};
-  cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_stride) * 2, static_cast<cuuint64_t>(page_stride) * 2};
-  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_stride) * es, static_cast<cuuint64_t>(page_stride) * es};
+  cuuint32_t box[3] = {e4m3 ? 128u : 64u, static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const CUresult r = fn(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+                        dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return set_error(LSA_ERR_CUDA, "cuTensorMapEncodeTiled (pages) failed (%d)", static_cast<int>(r));
   return LSA_OK;
@@ -403,21 +406,18 @@ lsa_status_t lsa_paged_attn(const lsa_paged_attn_in_t* in, void* out, float* lse
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   PagedMaps m{};
   if (is_mla(in)) {
-    if (in->kv_dtype == LSA_E4M3) {
-      a.kv8 = static_cast<const uint8_t*>(in->k);
-      a.kv8_page = in->k_page_stride; a.kv8_row = in->k_row_stride;
-      a.k_scale = in->k_scale;
-    } else if ((s = page_map(&m.k, in->k, 576, in->page_size, in->n_pages, in->k_row_stride, in->k_page_stride,
-                             std::min(in->page_size, kPagedBox))) != LSA_OK) {
+    const bool e4m3 = in->kv_dtype == LSA_E4M3;
+    if (e4m3) a.k_scale = in->k_scale;
+    if ((s = page_map(&m.k, in->k, e4m3, 576, in->page_size, in->n_pages, in->k_row_stride, in->k_page_stride,
+                      std::min(in->page_size, kPagedBox))) != LSA_OK)
       return s;
-    }
-    s = cuda_check(launch_paged_mla(m, a, st), "paged latent attention launch");
+    s = cuda_check(launch_paged_mla(m, a, e4m3, st), "paged latent attention launch");
   } else {
     const int box = std::min(in->page_size, kPagedBN);
-    if ((s = page_map(&m.k, in->k, in->Hkv * in->d_qk, in->page_size, in->n_pages, in->k_row_stride, in->k_page_stride,
+    if ((s = page_map(&m.k, in->k, false, in->Hkv * in->d_qk, in->page_size, in->n_pages, in->k_row_stride, in->k_page_stride,
                       box)) != LSA_OK)
       return s;
-    if ((s = page_map(&m.v, in->v, in->Hkv * in->d_v, in->page_size, in->n_pages, in->v_row_stride, in->v_page_stride,
+    if ((s = page_map(&m.v, in->v, false, in->Hkv * in->d_v, in->page_size, in->n_pages, in->v_row_stride, in->v_page_stride,
                       box)) != LSA_OK)
       return s;
     s = cuda_check(launch_paged_attn(m, a, in->d_qk, p.shared_kv, st), "paged attention launch");

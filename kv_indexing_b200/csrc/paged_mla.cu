@@ -35,8 +35,8 @@
 // the layout of the pair's accumulator); warps 4-7 load every fourth slot each
 // (TMA boxes of one page, or of the page's part of 64 keys; one warp alone issues
 // boxes at 7 TB/s over the GPU, two at 13, four at 19); the last warp of CTA 0
-// issues the MMAs. e4m3: warps 4-11 stage rows (codes -> bf16, exact) in place of
-// the loads; a key's scale multiplies its score and its P.
+// issues the MMAs. e4m3: warp 4 loads raw codes and warps 5-12 convert them
+// (codes -> bf16, exact); a key's scale multiplies its score and its P.
 //
 // The running maximum moves only when a block raises it by more than 2^8 (P in
 // bf16 keeps its relative precision, sums are fp32), so O is rescaled rarely.
@@ -58,22 +58,32 @@ constexpr int BN = kPagedBN;
 constexpr int kRows = 128;                       // rows of a tile, 64 per CTA
 constexpr int kChunk = 64 * 128;                 // 64 keys (or rows) x 64 columns, bytes
 constexpr int kSlot = 2 * kChunk;
-constexpr int kSlots = 10;
 constexpr int kPBytes = 2 * kChunk;              // 64 rows x 128 keys
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0, kColS = 256, kColQ = 320;
 constexpr int kTmemChunks = 6;                   // 64-column chunks of q in tensor memory, the rest in shared memory
 constexpr int kOffP = (9 - kTmemChunks) * kChunk;
 constexpr int kOffRing = kOffP + 2 * kPBytes;
-constexpr int kOffSwap = kOffRing + kSlots * kSlot;  // [2][128] what a row's two threads tell each other
-constexpr int kOffScale = kOffSwap + 2 * 128 * 4;     // e4m3: [4 warps][64] scales of the block's keys
-constexpr int kOffBars = kOffScale + 4 * 64 * 4;
-constexpr int kNumBars = 2 * kSlots + 13;   // full, empty, s_full, s_free, p_full[2], pv_done, o_full, q_full, tail[4], swap[2]
-constexpr int kOffWork = kOffBars + kNumBars * 8;
-constexpr int kOffMisc = kOffWork + sizeof(Work);
-constexpr size_t kSmem = 1024 + kOffMisc + 16;
-static_assert(kOffRing % 1024 == 0 && kOffScale % 16 == 0 && kOffBars % 8 == 0 && kOffWork % 8 == 0 && kSmem <= 227 * 1024,
-              "shared memory layout");
+
+// The ring, and for e4m3 a second one of raw codes (64 keys x 128 columns, 8 KB)
+// before it, deep enough for the loads; the converted slots then need little.
+template <bool KV8>
+struct Lay {
+  static constexpr int kSlots = KV8 ? 6 : 10, kRaw = KV8 ? 8 : 0;
+  static constexpr int kOffRaw = kOffRing + kSlots * kSlot;
+  static constexpr int kOffSwap = kOffRaw + kRaw * kChunk;       // [2][128] what a row's two threads tell each other
+  static constexpr int kOffScale = kOffSwap + 2 * 128 * 4;       // e4m3: [4 warps][64] scales of the block's keys
+  static constexpr int kOffBars = kOffScale + 4 * 64 * 4;
+  // full, empty, raw_full, raw_empty, s_full, s_free, p_full[2], pv_done, o_full, q_full, tail[4], swap[2]
+  static constexpr int kNumBars = 2 * kSlots + 2 * kRaw + 13;
+  static constexpr int kOffWork = kOffBars + kNumBars * 8;
+  static constexpr int kOffMisc = kOffWork + static_cast<int>(sizeof(Work));
+  static constexpr size_t kSmem = 1024 + kOffMisc + 16;
+  static constexpr int kMmaWarp = KV8 ? 13 : 8;
+  static constexpr int kThreads = (kMmaWarp + 1) * 32;
+  static_assert(kOffRing % 1024 == 0 && kOffRaw % 1024 == 0 && kOffScale % 16 == 0 && kOffBars % 8 == 0 && kOffWork % 8 == 0 &&
+                    kSmem <= 227 * 1024, "shared memory layout");
+};
 
 // Two of four e4m3 codes (the lower or the upper pair) -> a bf16 pair, exact:
 // the code's exponent and mantissa, moved to the low end of bf16's exponent and
@@ -89,20 +99,21 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t four) {
 }
 
 template <bool KV8>
-constexpr int threads_of() { return KV8 ? 416 : 288; }
-
-template <bool KV8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 1)
     paged_mla_kernel(const __grid_constant__ CUtensorMap tm_k, const PagedArgs a) {
+  using Y = Lay<KV8>;
+  constexpr int kSlots = Y::kSlots, kRaw = Y::kRaw, kMmaWarp = Y::kMmaWarp;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = base;
   uint8_t* sP = base + kOffP;
   uint8_t* sRing = base + kOffRing;
-  float* swap_s = reinterpret_cast<float*>(base + kOffSwap);
-  uint64_t* full = reinterpret_cast<uint64_t*>(base + kOffBars);   // CTA 0: both halves of a slot are there
+  float* swap_s = reinterpret_cast<float*>(base + Y::kOffSwap);
+  uint64_t* full = reinterpret_cast<uint64_t*>(base + Y::kOffBars);   // CTA 0: both halves of a slot are there
   uint64_t* empty = full + kSlots;
-  uint64_t* s_full = empty + kSlots;
+  uint64_t* raw_full = empty + kSlots;
+  uint64_t* raw_empty = raw_full + kRaw;
+  uint64_t* s_full = raw_empty + kRaw;
   uint64_t* s_free = s_full + 1;       // CTA 0: both CTAs have read the scores
   uint64_t* p_full = s_free + 1;       // [2], CTA 0: P of both CTAs is stored
   uint64_t* pv_done = p_full + 2;
@@ -110,10 +121,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
   uint64_t* q_full = o_full + 1;       // CTA 0
   uint64_t* tail = q_full + 1;         // [4] a slot that is cleared in part before it counts, by loading warp
   uint64_t* swap = tail + 4;           // [2] warps w and w + 2 have stored theirs
-  Work* work_s = reinterpret_cast<Work*>(base + kOffWork);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + kOffMisc);
+  Work* work_s = reinterpret_cast<Work*>(base + Y::kOffWork);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + Y::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  constexpr int kMmaWarp = KV8 ? 12 : 8;
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -122,8 +132,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&full[i], KV8 ? 16 : 2);
+      mbar_init(&full[i], KV8 ? 8 : 2);
       mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&raw_full[i], 1);
+      mbar_init(&raw_empty[i], 4);
     }
     mbar_init(s_full, 1);
     mbar_init(s_free, 8);
@@ -320,119 +334,121 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
         }
       }
     } else {
-      // --------------------------------------------- e4m3: stage the rows --
-      // A slot's 64 rows x 128 codes are read 16 bytes a lane, eight lanes to a
-      // row (a chunk alone: four). K's codes of a block are loaded while V's of
-      // the last one are converted, and the other way round.
-      const int t = tid - 128;
-      const int row = t >> 3, piece = t & 7;       // rows `row` and `row` + 32
-      const int row8 = t >> 2, piece8 = t & 3;     // chunk 8
-      int st = 0;
-      uint32_t ph = 1;
-      for (Work k = *work_s; ok && k.n > 0; next_work<kRows, BN>(a, k)) {
-        const int b = k.bt / a.tiles;
-        const Lens L = lens_of(a, b);
-        const int* trow = a.table + static_cast<long long>(b) * a.max_pages;
-        // lane g < 8: the table entry of the block's keys [16 g, 16 g + 16); looked at a block later
-        auto entry_of = [&](int j) -> int {
-          const int tok = (k.blk0 + j) * BN + lane * 16;
-          return lane < 8 && j < k.n && tok < L.len ? __ldg(trow + (tok >> a.page_shift)) : kNoPage;
-        };
-        auto page_of = [&](int p) -> int {
-          if (p >= 0 && p < a.n_pages) return p;
-          if (p != kNoPage && warp == 4) record_bad_page(a.status);
-          return -1;
-        };
-        // row `key` of block j, or null where nothing is to be read
-        auto row_of = [&](int j, int pages, int key) -> const uint4* {
-          const int page = __shfl_sync(0xffffffffu, pages, key >> 4);
-          const int tok = (k.blk0 + j) * BN + key;
-          if (page < 0 || tok >= L.len) return nullptr;
-          return reinterpret_cast<const uint4*>(a.kv8 + page * a.kv8_page + (tok & ((1 << a.page_shift) - 1)) * a.kv8_row);
-        };
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        uint4 vk[9], vv[8];
-        auto load_k = [&](int j, int pages) {
-          const uint4* r0 = row_of(j, pages, rank * 64 + row);
-          const uint4* r1 = row_of(j, pages, rank * 64 + row + 32);
-          const uint4* r8 = row_of(j, pages, rank * 64 + row8);
-#pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            vk[2 * s] = r0 ? __ldg(r0 + s * 8 + piece) : zero;
-            vk[2 * s + 1] = r1 ? __ldg(r1 + s * 8 + piece) : zero;
+      uint8_t* sRaw = base + Y::kOffRaw;
+      if (warp == 4) {
+        // ------------------------------------------- e4m3: raw codes --
+        const int box = min(kPagedBox, 1 << a.page_shift), per = 64 / box;
+        int rs = 0;
+        uint32_t ph = 1;                                         // the ring starts empty
+        for (Work k = *work_s; ok && k.n > 0; next_work<kRows, BN>(a, k)) {
+          const int b = k.bt / a.tiles;
+          const Lens L = lens_of(a, b);
+          const int* trow = a.table + static_cast<long long>(b) * a.max_pages;
+          // lane g < 8: the table entry of the block's keys [16 g, 16 g + 16); looked at a block later
+          auto entry_of = [&](int j) -> int {
+            const int tok = (k.blk0 + j) * BN + lane * 16;
+            return lane < 8 && j < k.n && tok < L.len ? __ldg(trow + (tok >> a.page_shift)) : kNoPage;
+          };
+          auto page_of = [&](int p) -> int {
+            if (p >= 0 && p < a.n_pages) return p;
+            if (p != kNoPage) record_bad_page(a.status);
+            return -1;
+          };
+          // 64 keys from `key` of block j, 128 codes from `col`
+          auto load = [&](int j, int pages, int key, int col) -> bool {
+            if (!__all_sync(0xffffffffu, wait(&raw_empty[rs], ph, a.status, abort_flag))) return false;
+            const int tok = (k.blk0 + j) * BN + key;
+            const int page = __shfl_sync(0xffffffffu, pages, ((key + lane * box) >> 4) & 31);
+            if (lane == 0) mbar_arrive_expect_tx(&raw_full[rs], kChunk);
+            __syncwarp();
+            if (lane < per)
+              tma_load_page(sRaw + rs * kChunk + lane * box * 128, &tm_k, &raw_full[rs], col,
+                            (tok + lane * box) & ((1 << a.page_shift) - 1), page >= 0 ? page : a.n_pages);
+            if (++rs == kRaw) {
+              rs = 0;
+              ph ^= 1u;
+            }
+            return true;
+          };
+          auto load_k = [&](int j, int pages) -> bool {
+#pragma unroll 1
+            for (int s = 0; s < 5; ++s)                          // the last one half past the row's end: zeros
+              if (!load(j, pages, rank * 64, s * 128)) return false;
+            return true;
+          };
+          auto load_v = [&](int j, int pages) -> bool {
+#pragma unroll 1
+            for (int s = 0; s < 4; ++s)
+              if (!load(j, pages, (s >> 1) * 64, (s & 1) * 256 + rank * 128)) return false;
+            return true;
+          };
+          int cur = page_of(entry_of(0)), entry = entry_of(1);
+          ok = load_k(0, cur);
+          for (int j = 0; ok && j < k.n; ++j) {
+            const int nxt = page_of(entry);
+            entry = entry_of(j + 2);
+            if (j + 1 < k.n) ok = load_k(j + 1, nxt);
+            if (ok) ok = load_v(j, cur);
+            cur = nxt;
           }
-          vk[8] = r8 ? __ldg(r8 + 32 + piece8) : zero;
-        };
-        auto load_v = [&](int j, int pages) {
+        }
+      } else {
+        // --------------------------- e4m3: codes -> bf16, into the ring --
+        // Two groups of four warps take alternate slots, one code path for all of
+        // them (a path for K and one for V, with their codes in registers, ran at
+        // a sixth of an instruction a cycle). A lane converts 8 codes at a time;
+        // odd rows take a slot's chunks the other way round, so that two rows'
+        // reads do not meet in a bank.
+        const uint32_t group = (warp - 5) >> 2;
+        const int t = (tid - 160) & 127;
+        const int row = t >> 3, unit = t & 7;                    // rows row + 16 i
+        uint32_t seq = 0;                                        // slots before the piece
+        for (Work k = *work_s; ok && k.n > 0; next_work<kRows, BN>(a, k)) {
+          const Lens L = lens_of(a, k.bt / a.tiles);
+          const uint32_t n = 9 * k.n;
+#pragma unroll 1
+          for (uint32_t i = (seq & 1) ^ group; i < n; i += 2) {
+            // the ring takes K(0), then K(j + 1) (while there is one) and V(j) in turn
+            int rows = 64, chunks = 2;                           // rows that count (V), chunks of the slot
+            if (i == 4) {
+              chunks = 1;
+            } else if (i > 4) {
+              const int q = i - 5, j = q / 9, s = q - 9 * j;
+              const bool last = j + 1 == k.n;
+              if (!last && s < 5) {
+                if (s == 4) chunks = 1;
+              } else {
+                const int half = (last ? s : s - 5) >> 1;
+                rows = L.len - (k.blk0 + j) * BN - half * 64;
+              }
+            }
+            const uint32_t at = seq + i, rs = at % kRaw, st = at % kSlots;
+            ok = __all_sync(0xffffffffu, wait(&raw_full[rs], (at / kRaw) & 1, a.status, abort_flag) &&
+                                             wait(&empty[st], ((at / kSlots) & 1) ^ 1, a.status, abort_flag));
+            if (!ok) break;
+            const uint8_t* src = sRaw + rs * kChunk;
+            uint8_t* dst = sRing + st * kSlot;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4* r0 = row_of(j, pages, h * 64 + row);
-            const uint4* r1 = row_of(j, pages, h * 64 + row + 32);
+            for (int r4 = 0; r4 < 4; ++r4) {
+              const int r = row + 16 * r4;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              vv[4 * h + 2 * n] = r0 ? __ldg(r0 + n * 16 + rank * 8 + piece) : zero;
-              vv[4 * h + 2 * n + 1] = r1 ? __ldg(r1 + n * 16 + rank * 8 + piece) : zero;
+              for (int cc = 0; cc < 2; ++cc) {
+                const int c = cc ^ (row & 1);
+                if (c >= chunks) continue;
+                uint2 e = *reinterpret_cast<const uint2*>(src + r * 128 + c * 64 + unit * 8);
+                if (r >= rows) e = make_uint2(0u, 0u);           // past seq_len, whatever the page holds
+                *reinterpret_cast<uint4*>(dst + c * kChunk + r * 128 + ((unit ^ (r & 7)) << 4)) =
+                    make_uint4(codes_to_bf16<0>(e.x), codes_to_bf16<1>(e.x), codes_to_bf16<0>(e.y), codes_to_bf16<1>(e.y));
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&raw_empty[rs]);
+              mbar_arrive_at(full0 + st * 8);
             }
           }
-        };
-        // 16 codes -> two 16-byte units of a chunk's row; `flip`: the upper one first, so that the lanes of two chunks
-        // do not meet in a bank
-        auto put = [&](uint8_t* chunk, int r, int unit, const uint4& e, bool flip) {
-          uint8_t* dst = chunk + r * 128;
-          const uint4 lo = make_uint4(codes_to_bf16<0>(e.x), codes_to_bf16<1>(e.x), codes_to_bf16<0>(e.y), codes_to_bf16<1>(e.y));
-          const uint4 hi = make_uint4(codes_to_bf16<0>(e.z), codes_to_bf16<1>(e.z), codes_to_bf16<0>(e.w), codes_to_bf16<1>(e.w));
-          *reinterpret_cast<uint4*>(dst + (((unit + flip) ^ (r & 7)) << 4)) = flip ? hi : lo;
-          *reinterpret_cast<uint4*>(dst + (((unit + !flip) ^ (r & 7)) << 4)) = flip ? lo : hi;
-        };
-        auto emit = [&](const uint4& e0, const uint4& e1, bool two) -> bool {
-          if (!__all_sync(0xffffffffu, wait(&empty[st], ph, a.status, abort_flag))) return false;
-          uint8_t* dst = sRing + st * kSlot;
-          if (two) {
-            put(dst + (piece >> 2) * kChunk, row, (piece & 3) * 2, e0, piece >> 2);
-            put(dst + (piece >> 2) * kChunk, row + 32, (piece & 3) * 2, e1, piece >> 2);
-          } else {
-            put(dst, row8, piece8 * 2, e0, row8 & 1);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(full0 + st * 8);
-          if (++st == kSlots) {
-            st = 0;
-            ph ^= 1u;
-          }
-          return true;
-        };
-        auto emit_k = [&]() -> bool {
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            if (!emit(vk[2 * s], vk[2 * s + 1], true)) return false;
-          return emit(vk[8], vk[8], false);
-        };
-        auto emit_v = [&]() -> bool {
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            if (!emit(vv[2 * s], vv[2 * s + 1], true)) return false;
-          return true;
-        };
-        int pages = page_of(entry_of(0));
-        int entry = entry_of(1);
-        load_k(0, pages);
-        load_v(0, pages);
-        int next = page_of(entry);
-        entry = entry_of(2);
-        ok = emit_k();
-        load_k(1, next);
-        for (int j = 0; ok && j < k.n; ++j) {
-          const int after = page_of(entry);
-          entry = entry_of(j + 3);
-          if (j + 1 < k.n) {
-            ok = emit_k();
-            if (!ok) break;
-          }
-          load_k(j + 2, after);
-          ok = emit_v();
-          load_v(j + 1, next);
-          next = after;
+          seq += n;
         }
       }
     }
@@ -442,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t p_full0 = mapa_shared(smem_u32(p_full), 0), q_full0 = mapa_shared(smem_u32(q_full), 0);
     const uint32_t s_free0 = mapa_shared(smem_u32(s_free), 0);
-    float* scale_s = reinterpret_cast<float*>(base + kOffScale) + warp * 64;
+    float* scale_s = reinterpret_cast<float*>(base + Y::kOffScale) + warp * 64;
     const float c = a.scale_log2;
     uint32_t jb = 0, seg = 0, n_swap = 0;
     // Tells the row's other thread v and returns its value (through alternate buffers: a value is read before the
@@ -712,14 +728,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<KV8>(), 1
 
 }  // namespace
 
-cudaError_t launch_paged_mla(const PagedMaps& m, const PagedArgs& a, cudaStream_t stream) {
-  const bool kv8 = a.kv8 != nullptr;
-  const void* fn = kv8 ? reinterpret_cast<const void*>(&paged_mla_kernel<true>)
-                       : reinterpret_cast<const void*>(&paged_mla_kernel<false>);
-  const cudaError_t e = set_max_smem(fn, kSmem);
+template <bool KV8>
+static cudaError_t launch_mla_t(const PagedMaps& m, const PagedArgs& a, cudaStream_t stream) {
+  const void* fn = reinterpret_cast<const void*>(&paged_mla_kernel<KV8>);
+  const cudaError_t e = set_max_smem(fn, Lay<KV8>::kSmem);
   if (e != cudaSuccess) return e;
   void* args[] = {const_cast<CUtensorMap*>(&m.k), const_cast<PagedArgs*>(&a)};
-  return launch_pdl(fn, dim3(2 * a.workers), dim3(kv8 ? threads_of<true>() : threads_of<false>()), kSmem, stream, args);
+  return launch_pdl(fn, dim3(2 * a.workers), dim3(Lay<KV8>::kThreads), Lay<KV8>::kSmem, stream, args);
+}
+
+cudaError_t launch_paged_mla(const PagedMaps& m, const PagedArgs& a, int e4m3, cudaStream_t stream) {
+  return e4m3 ? launch_mla_t<true>(m, a, stream) : launch_mla_t<false>(m, a, stream);
 }
 
 }  // namespace lsa
