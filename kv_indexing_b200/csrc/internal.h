@@ -272,7 +272,7 @@ struct PagedMaps {
   CUtensorMap k, v;
 };
 constexpr int kPagedBN = 128;      // keys per block
-constexpr int kPagedBox = 64;      // most rows of a box, latent rows
+constexpr int kPagedBox = 64;      // most rows of a box
 constexpr int kMaxWorkers = 160;   // a merge keeps one weight per worker
 cudaError_t launch_paged_attn(const PagedMaps& m, const PagedArgs& a, int d, int shared_kv, cudaStream_t stream);
 cudaError_t launch_paged_mla(const PagedMaps& m, const PagedArgs& a, int e4m3, cudaStream_t stream);

@@ -413,7 +413,7 @@ lsa_status_t lsa_paged_attn(const lsa_paged_attn_in_t* in, void* out, float* lse
       return s;
     s = cuda_check(launch_paged_mla(m, a, e4m3, st), "paged latent attention launch");
   } else {
-    const int box = std::min(in->page_size, kPagedBN);
+    const int box = std::min(in->page_size, kPagedBox);
     if ((s = page_map(&m.k, in->k, false, in->Hkv * in->d_qk, in->page_size, in->n_pages, in->k_row_stride, in->k_page_stride,
                       box)) != LSA_OK)
       return s;

@@ -10,19 +10,26 @@
 // A block works on two row tiles in turn, so that the tensor cores compute one
 // tile's products while the other's softmax runs:
 //   SHARED = 1 (more than 128 rows): two tiles of 128 rows over the same keys;
-//   SHARED = 0 (a few rows): one tile of rows, the two halves taking the even
-//     and the odd key blocks of a piece, each with its own maximum, sum and
-//     output; half 1 hands its output to half 0 through shared memory.
+//   SHARED = 0 (a few rows): one tile of rows, the two halves taking a piece's
+//     keys 64 by 64 in turn, each with its own maximum, sum and output; half 1
+//     hands its output to half 0 through shared memory.
 //
 // A block works through the pieces of the work list (paged.cuh) that are its.
 //
 // Threads (352): warps 0-3 and 4-7 are the softmax of the two halves, one
-// thread per row; warps 8 and 10 load K and V pages by TMA into a ring of
-// 128-key tiles (boxes of one page, or of the page's part of the block; one warp
-// alone issues boxes more slowly than HBM delivers them); warp 9 issues the MMAs. Scores (128 columns) and O (d columns) of both halves fill tensor
-// memory; P (bf16) overwrites the scores it came from and is the A operand of
-// the second MMA. MMAs issued by one thread run in order, so a half's next
-// scores cannot overtake the product that reads its P.
+// thread per row; warps 8 and 10 load K and V pages by TMA into a ring of 64-key
+// tiles (boxes of one page, or of the page's part of the tile; one warp alone
+// issues boxes more slowly than HBM delivers them); one thread of warp 9 issues
+// the MMAs.
+//
+// A step is 64 keys, one K and one V tile. Two scores' buffers of 64 columns and
+// O (d columns) for each half fill tensor memory: the scores of step u + 1 are
+// computed while the softmax of step u runs. P (bf16) overwrites the scores it
+// came from and is the A operand of the second MMA. MMAs issued by one thread
+// run in order, so scores cannot overtake the product that reads the buffer's
+// last P. (With steps of 128 keys and one buffer the products waited for the
+// softmax and it for them, 4100 cycles for 128 keys of 256 rows; a score product
+// of 64 keys takes 1.5 times its share, bound by shared memory, and still wins.)
 //
 // The running maximum only moves when a block raises it by more than 2^8 (the
 // bf16 P keeps its relative precision, sums are fp32), so O is rescaled rarely.
@@ -40,19 +47,20 @@ using namespace paged;
 
 constexpr int kSoft = 256;             // softmax threads
 constexpr int kThreads = 352;
-constexpr int BN = kPagedBN;
+constexpr int BN = kPagedBN;           // keys of a block of the work list
+constexpr int kStep = 64;              // keys of a step
 
 template <int D, bool SHARED>
 struct Cfg {
   static constexpr int kChunks = D / 64;
   static constexpr int kQTile = 128 * D * 2;
   static constexpr int kQTiles = SHARED ? 2 : 1;
-  static constexpr int kStage = BN * D * 2;
-  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kStage = kStep * D * 2;
+  static constexpr int kStages = D == 128 ? 10 : 20;   // at least six: half 1's next scores are issued before half 0's product
   static constexpr int kOffStage = kQTiles * kQTile;
   static constexpr int kOffMask = kOffStage + kStages * kStage;
   static constexpr int kOffBars = kOffMask + ((kStages * 4 + 7) / 8) * 8;
-  static constexpr int kNumBars = 2 * kStages + 9;
+  static constexpr int kNumBars = 2 * kStages + 15;
   static constexpr int kOffWork = kOffBars + kNumBars * 8;
   static constexpr int kOffMerge = (kOffWork + 9 * static_cast<int>(sizeof(Work)) + 15) / 16 * 16;   // the block's, and the softmax warps'
   static constexpr int kMergeRow = 36;                 // floats: 32 columns, padded
@@ -60,7 +68,7 @@ struct Cfg {
   static constexpr size_t kSmem = 1024 + kOffMisc + 16;
 };
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;   // S of half i at 128 i, O at 256 + D i
+constexpr uint32_t kColS = 0, kColO = 256;   // S of half i, buffer e at 128 i + 64 e, O at 256 + D i
 
 template <int D, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -72,13 +80,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = base;
   uint8_t* sStage = base + C::kOffStage;
-  uint32_t* mask_s = reinterpret_cast<uint32_t*>(base + C::kOffMask);   // [kStages] mapped pages of a V tile
+  uint32_t* mask_s = reinterpret_cast<uint32_t*>(base + C::kOffMask);   // [kStages] of a V tile: which 16 keys have a page
   uint64_t* bars = reinterpret_cast<uint64_t*>(base + C::kOffBars);
   uint64_t* kv_full = bars;
   uint64_t* kv_empty = bars + C::kStages;
-  uint64_t* s_full = bars + 2 * C::kStages;   // [2]
-  uint64_t* p_full = s_full + 2;              // [2]
-  uint64_t* o_full = p_full + 2;              // [2]
+  uint64_t* s_full = bars + 2 * C::kStages;   // [2 halves][2 buffers]
+  uint64_t* p_full = s_full + 4;              // [2][2]
+  uint64_t* pv_done = p_full + 4;             // [2]
+  uint64_t* o_full = pv_done + 2;             // [2] the piece's last product
   uint64_t* q_full = o_full + 2;
   uint64_t* mg_full = q_full + 1;             // half 1's columns are in the merge buffer / have been read
   uint64_t* mg_empty = mg_full + 1;
@@ -97,9 +106,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&kv_full[i], 1);
       mbar_init(&kv_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 128);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&pv_done[i], 1);
       mbar_init(&o_full[i], 1);
     }
     mbar_init(q_full, kSoft);
@@ -138,122 +150,129 @@ __global__ void __launch_bounds__(kThreads, 1)
     p.len = L.len;
     p.rows = L.n_new * a.G;
     p.first_pos = L.len - L.n_new;             // position of token t: first_pos + t
+    // steps of the piece that the last of the rows [r0, r0 + n) sees
+    auto steps = [&](int r0, int n) -> int {
+      if (r0 >= p.rows) return 0;
+      const int keys = max(0, min(L.len, p.first_pos + (min(p.rows, r0 + n) - 1) / a.G + 1));
+      return max(0, min(k.n * (BN / kStep), (keys + kStep - 1) / kStep - k.blk0 * (BN / kStep)));
+    };
     if (SHARED) {
-      // key blocks that the last row of half i's tile sees
-      auto blocks = [&](int r0) -> int {
-        if (r0 >= p.rows) return 0;
-        return (max(0, min(L.len, p.first_pos + (min(p.rows, r0 + 128) - 1) / a.G + 1)) + BN - 1) / BN;
-      };
-      const int end = k.blk0 + k.n;
-      p.n0 = max(0, min(end, blocks(p.row0)) - k.blk0);
-      p.n1 = max(0, min(end, blocks(p.row0 + 128)) - k.blk0);
+      p.n0 = steps(p.row0, 128);
+      p.n1 = steps(p.row0 + 128, 128);
     } else {
-      p.n0 = (k.n + 1) / 2;
-      p.n1 = k.n / 2;
+      const int n = steps(p.row0, 128);
+      p.n0 = (n + 1) / 2;
+      p.n1 = n / 2;
     }
     return p;
   };
-  // key blocks that are loaded
-  auto n_blk_of = [&](const Piece& p) -> int { return SHARED ? max(p.n0, p.n1) : p.n0 + p.n1; };
-  // place in the ring, from the piece's first tile on, of the K tile of half i's step s (its V tile follows)
-  auto seq_of = [&](int i, int s) -> int { return SHARED ? 2 * s : 2 * (2 * s + i); };
+  // tiles of K (and of V) that are loaded
+  auto n_tiles_of = [&](const Piece& p) -> int { return SHARED ? max(p.n0, p.n1) : p.n0 + p.n1; };
+  // tile of half i's step u; its K and V follow one another in the ring
+  auto tile_of = [&](int i, int u) -> int { return SHARED ? u : 2 * u + i; };
 
   if (warp == 8 || warp == 10) {
     // ------------------------------------------------ producers (K and V) --
     const uint32_t kv = warp == 10;
-    const int per = BN >> a.page_shift;        // pages of a block (page sizes up to 128)
+    const int box = min(kStep, 1 << a.page_shift), per = kStep / box;   // rows of a box, boxes of 64 columns
     const int n_ops = C::kChunks * per;
     const int j = lane % per, c = lane / per;
-    const int rows_box = 1 << a.page_shift;
+    const uint32_t groups = (1u << (box / 16)) - 1u;
     uint32_t seq = 0;
     for (Work k = *work_s; ok && k.n > 0; next_work<kTile, BN>(a, k)) {
       const Piece p = piece_of(k);
-      const int n_blk = n_blk_of(p);
+      const int n_tiles = n_tiles_of(p), first = k.blk0 * BN + j * box;
       const int* row = a.table + static_cast<long long>(p.b) * a.max_pages;
-      auto page_of = [&](int blk) -> int {     // physical page of this lane's page of the block
-        const int tok = (k.blk0 + blk) * BN + (j << a.page_shift);
-        return blk < n_blk && tok < p.len ? __ldg(row + (tok >> a.page_shift)) : kNoPage;
+      auto page_of = [&](int tile) -> int {    // physical page of this lane's box of the tile
+        const int tok = first + tile * kStep;
+        return tile < n_tiles && tok < p.len ? __ldg(row + (tok >> a.page_shift)) : kNoPage;
       };
       int next = page_of(0);
-      for (int blk = 0; ok && blk < n_blk; ++blk) {
+      for (int tile = 0; ok && tile < n_tiles; ++tile) {
         int page = next;
-        next = page_of(blk + 1);               // not looked at before the next block: the load takes its time
+        next = page_of(tile + 1);              // not looked at before the next tile: the load takes its time
         if (page < 0 || page >= a.n_pages) {
           if (page != kNoPage && c == 0 && kv == 0) record_bad_page(a.status);
           page = -1;
         }
-        const uint32_t mapped = __ballot_sync(0xffffffffu, page >= 0) & ((1u << per) - 1u);
-        const uint32_t at = seq + 2 * blk + kv, st = at % C::kStages;
+        uint32_t mapped = __ballot_sync(0xffffffffu, page >= 0);
+        const uint32_t at = seq + 2 * tile + kv, st = at % C::kStages;
         ok = __all_sync(0xffffffffu, wait(&kv_empty[st], ((at / C::kStages) & 1) ^ 1, a.status, abort_flag));
         if (!ok) break;
         if (lane == 0) {
-          if (kv) mask_s[st] = mapped;
+          if (kv) {
+            uint32_t m = 0u;
+            for (int i = 0; i < per; ++i, mapped >>= 1) m |= (mapped & 1u ? groups : 0u) << (i * (box / 16));
+            mask_s[st] = m;
+          }
           mbar_arrive_expect_tx(&kv_full[st], C::kStage);
         }
         __syncwarp();
         if (lane < n_ops)
-          tma_load_page(sStage + st * C::kStage + c * (BN * 128) + j * rows_box * 128, kv ? &tm_v : &tm_k, &kv_full[st],
-                        p.g * D + c * 64, 0, page >= 0 ? page : a.n_pages);
+          tma_load_page(sStage + st * C::kStage + c * (kStep * 128) + j * box * 128, kv ? &tm_v : &tm_k, &kv_full[st],
+                        p.g * D + c * 64, (first + tile * kStep) & ((1 << a.page_shift) - 1), page >= 0 ? page : a.n_pages);
       }
-      seq += 2 * n_blk;
+      seq += 2 * n_tiles;
     }
   } else if (warp == 9) {
     // -------------------------------------------------------- MMA issuer --
-    const uint32_t idesc_qk = make_idesc(1, 1, 128, BN, 0, 0);
-    const uint32_t idesc_pv = make_idesc(1, 1, 128, D, 0, 1);
-    const uint64_t dQ = make_sdesc(smem_u32(sQ), 16, 1024, kLayoutSW128);
-    const uint64_t dK = make_sdesc(smem_u32(sStage), 16, 1024, kLayoutSW128);
-    const uint64_t dV = make_sdesc(smem_u32(sStage), BN * 128, 1024, kLayoutSW128);
-    uint32_t seq0 = 0, seg = 0, done0 = 0, done1 = 0;        // ring places, pieces, steps of the halves before this piece
-    for (Work k = *work_s; ok && k.n > 0; next_work<kTile, BN>(a, k), ++seg) {
-      const Piece p = piece_of(k);
-      const int n0 = p.n0, n1 = p.n1;
-      auto full = [&](uint32_t seq) { return wait(&kv_full[seq % C::kStages], (seq / C::kStages) & 1, a.status, abort_flag); };
-      auto qk = [&](int i, int s) -> bool {
-        const uint32_t seq = seq0 + seq_of(i, s), st = seq % C::kStages;
-        if (!full(seq)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t q0 = dQ + (SHARED ? i * (C::kQTile / 16) : 0), k0 = dK + st * (C::kStage / 16);
+    if (elect_one()) {
+      const uint32_t idesc_qk = make_idesc(1, 1, 128, kStep, 0, 0);
+      const uint32_t idesc_pv = make_idesc(1, 1, 128, D, 0, 1);
+      const uint32_t hi = static_cast<uint32_t>(make_sdesc(0, 16, 1024, kLayoutSW128) >> 32);
+      const uint32_t dQ = static_cast<uint32_t>(make_sdesc(smem_u32(sQ), 16, 1024, kLayoutSW128));
+      const uint32_t dK = static_cast<uint32_t>(make_sdesc(smem_u32(sStage), 16, 1024, kLayoutSW128));
+      const uint32_t dV = static_cast<uint32_t>(make_sdesc(smem_u32(sStage), kStep * 128, 1024, kLayoutSW128));
+      uint32_t seq0 = 0, seg = 0, done0 = 0, done1 = 0;      // ring places, pieces, steps of the halves before this piece
+      for (Work k = *work_s; ok && k.n > 0; next_work<kTile, BN>(a, k), ++seg) {
+        const Piece p = piece_of(k);
+        const int n0 = p.n0, n1 = p.n1;
+        auto full = [&](uint32_t seq) { return wait(&kv_full[seq % C::kStages], (seq / C::kStages) & 1, a.status, abort_flag); };
+        auto qk = [&](int i, int u) -> bool {
+          const uint32_t seq = seq0 + 2 * tile_of(i, u), st = seq % C::kStages, e = ((i ? done1 : done0) + u) & 1;
+          if (!full(seq)) return false;
+          tc_fence_after();
+          const uint32_t q0 = dQ + (SHARED ? i * (C::kQTile / 16) : 0), k0 = dK + st * (C::kStage / 16);
+          const uint32_t d = tmem + kColS + 128 * i + kStep * e;
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_f16(tmem + kColS + 128 * i, q0 + c * 1024 + ks * 2, k0 + c * (BN * 8) + ks * 2, idesc_qk, (c | ks) ? 1u : 0u);
-          umma_commit(&s_full[i]);
-          if (!SHARED || i == 1 || s >= n1) umma_commit(&kv_empty[st]);
-        }
-        __syncwarp();
-        return true;
-      };
-      auto pv = [&](int i, int s) -> bool {
-        const uint32_t seq = seq0 + seq_of(i, s) + 1, st = seq % C::kStages;
-        if (!wait(&p_full[i], ((i ? done1 : done0) + s) & 1, a.status, abort_flag) || !full(seq)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t v0 = dV + st * (C::kStage / 16);
+              umma_f16_lo(d, q0 + c * 1024 + ks * 2, k0 + c * (kStep * 8) + ks * 2, hi, idesc_qk, (c | ks) ? 1u : 0u);
+          umma_commit(&s_full[2 * i + e]);
+          if (!SHARED || i == 1 || u >= n1) umma_commit(&kv_empty[st]);
+          return true;
+        };
+        auto pv = [&](int i, int u) -> bool {
+          const uint32_t seq = seq0 + 2 * tile_of(i, u) + 1, st = seq % C::kStages, at = (i ? done1 : done0) + u, e = at & 1;
+          if (!wait(&p_full[2 * i + e], (at >> 1) & 1, a.status, abort_flag) || !full(seq)) return false;
+          tc_fence_after();
+          const uint32_t v0 = dV + st * (C::kStage / 16);
 #pragma unroll
-          for (int ks = 0; ks < BN / 16; ++ks)
-            umma_f16_ts(tmem + kColO + D * i, tmem + kColS + 128 * i + ks * 8, v0 + ks * 128, idesc_pv, (s | ks) ? 1u : 0u);
-          if (!SHARED || i == 1 || s >= n1) umma_commit(&kv_empty[st]);
-          if (s + 1 == (i ? n1 : n0)) umma_commit(&o_full[i]);
+          for (int ks = 0; ks < kStep / 16; ++ks)
+            umma_f16_ts_lo(tmem + kColO + D * i, tmem + kColS + 128 * i + kStep * e + ks * 8, v0 + ks * 128, hi, idesc_pv,
+                           (u | ks) ? 1u : 0u);
+          umma_commit(&pv_done[i]);
+          if (!SHARED || i == 1 || u >= n1) umma_commit(&kv_empty[st]);
+          if (u + 1 == (i ? n1 : n0)) umma_commit(&o_full[i]);
+          return true;
+        };
+        ok = wait(q_full, seg & 1, a.status, abort_flag);
+        if (ok && n0 > 0) ok = qk(0, 0);
+        if (ok && n1 > 0) ok = qk(1, 0);
+        const int n = max(n0, n1);
+        for (int u = 0; ok && u < n; ++u) {
+          if (u + 1 < n0) ok = qk(0, u + 1);
+          if (ok && u + 1 < n1) ok = qk(1, u + 1);
+          if (ok && u < n0) ok = pv(0, u);
+          if (ok && u < n1) ok = pv(1, u);
         }
-        __syncwarp();
-        return true;
-      };
-      ok = wait(q_full, seg & 1, a.status, abort_flag);
-      if (ok && n0 > 0) ok = qk(0, 0);
-      const int n = max(n0, n1);
-      for (int s = 0; ok && s < n; ++s) {
-        if (s < n1) ok = qk(1, s);
-        if (ok && s < n0) ok = pv(0, s);
-        if (ok && s + 1 < n0) ok = qk(0, s + 1);
-        if (ok && s < n1) ok = pv(1, s);
+        seq0 += 2 * n_tiles_of(p);
+        done0 += n0;
+        done1 += n1;
       }
-      seq0 += 2 * n_blk_of(p);
-      done0 += n0;
-      done1 += n1;
     }
+    __syncwarp();
   } else {
     // ----------------------------------------------------------- softmax --
     const int half = warp >> 2;
@@ -278,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       len = p.len;
       rbase = p.row0 + (SHARED ? 128 * half : 0);
       n_steps = half ? p.n1 : p.n0;
-      n_places = 2 * n_blk_of(p);
+      n_places = 2 * n_tiles_of(p);
       blk0 = k.blk0;
       // keys this row sees; rows that do not exist see all, so that they make no block a masked one
       bound = rbase + rt < rows ? max(0, min(len, p.first_pos + (rbase + rt) / a.G + 1)) : len;
@@ -309,110 +328,97 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool idle = rbase + (warp & 3) * 32 >= rows;   // no row of this warp exists: its P and O are never used
     // nothing past the sequence's end may reach the product: the V rows there are cleared
     auto clear_tail = [&](uint32_t seq_v, int key0) {
-      if (key0 + BN <= len) return;
+      if (key0 + kStep <= len) return;
       uint8_t* vt = sStage + (seq_v % C::kStages) * C::kStage;
       const int z0 = max(0, len - key0);
 #pragma unroll 1
-      for (int i = rt; i < (BN - z0) * C::kChunks * 8; i += 128) {
+      for (int i = rt; i < (kStep - z0) * C::kChunks * 8; i += 128) {
         const int row = z0 + i / (C::kChunks * 8), u = i % (C::kChunks * 8);
-        *reinterpret_cast<uint4*>(vt + (u >> 3) * (BN * 128) + row * 128 + (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(vt + (u >> 3) * (kStep * 128) + row * 128 + (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
       }
       fence_proxy_async_smem();
     };
     float m_run = -INFINITY, l_run = 0.f;       // log2 domain
-    if (idle) {
-      for (int s = 0; ok && s < n_steps; ++s) {
-        const uint32_t seq_v = seq0 + seq_of(half, s) + 1;
-        ok = __all_sync(0xffffffffu, wait(&s_full[half], (done + s) & 1, a.status, abort_flag) &&
-                                         wait(&kv_full[seq_v % C::kStages], (seq_v / C::kStages) & 1, a.status, abort_flag));
-        if (!ok) break;
-        clear_tail(seq_v, (blk0 + (SHARED ? s : 2 * s + half)) * BN);
-        mbar_arrive(&p_full[half]);
-      }
-    } else
-    for (int s = 0; s < n_steps; ++s) {
-      const uint32_t seq_v = seq0 + seq_of(half, s) + 1;
-      const int key0 = (blk0 + (SHARED ? s : 2 * s + half)) * BN;
-      ok = __all_sync(0xffffffffu, wait(&s_full[half], (done + s) & 1, a.status, abort_flag));
-      if (!ok) break;
-      // the V tile's barrier also publishes the block's mapped pages
-      ok = __all_sync(0xffffffffu, wait(&kv_full[seq_v % C::kStages], (seq_v / C::kStages) & 1, a.status, abort_flag));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t mapped = mask_s[seq_v % C::kStages];
-      const int vis = bound - key0;             // visible columns of this block
-      const bool masked = __any_sync(0xffffffffu, vis < BN) || mapped != (1u << (BN >> a.page_shift)) - 1u;
-      // The scores are read twice, for their maximum and for P: held in registers between, they would spill.
-      auto mask = [&](uint32_t (&v)[32], int q) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (32 * q + j >= vis || !((mapped >> ((32 * q + j) >> a.page_shift)) & 1u)) v[j] = 0xFF800000u;
-      };
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      {
-        uint32_t v0[32], v1[32];
-#pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          tmem_ld32(tS + 32 * q, v0);
-          tmem_ld32(tS + 32 * q + 32, v1);
-          tmem_ld_wait();
-          if (masked) {
-            mask(v0, q);
-            mask(v1, q + 1);
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) mx[j & 3] = max3(mx[j & 3], __uint_as_float(v0[j]), __uint_as_float(v1[j]));
-        }
-      }
-      const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-      const bool move = mb > m_run + 8.f || (m_run == -INFINITY && mb != -INFINITY);
-      float corr = 1.f;
-      if (move) {
-        corr = m_run == -INFINITY ? 0.f : ex2(m_run - mb);
-        l_run *= corr;
-        m_run = mb;
-      }
-      // this half's product of step s - 1 was issued before the scores of step s, and has completed with them
-      if (s > 0 && __any_sync(0xffffffffu, move)) {
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t ov[32];
-          tmem_ld32(tO + c0, ov);
+    for (int u = 0; u < n_steps; ++u) {
+      const uint32_t at = done + u, e = at & 1;
+      const int tile = tile_of(half, u), key0 = blk0 * BN + tile * kStep;
+      const uint32_t seq_v = seq0 + 2 * tile + 1;
+      // the V tile's barrier also publishes the tile's mapped pages
+      ok = __all_sync(0xffffffffu, wait(&s_full[2 * half + e], (at >> 1) & 1, a.status, abort_flag) &&
+                                       wait(&kv_full[seq_v % C::kStages], (seq_v / C::kStages) & 1, a.status, abort_flag));
+      if (!ok) break;
+      if (!idle) {
+        tc_fence_after();
+        const uint32_t tSe = tS + kStep * e;
+        float x[64];
+        {
+          uint32_t v0[32], v1[32];
+          tmem_ld32(tSe, v0);
+          tmem_ld32(tSe + 32, v1);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * corr);
-          tmem_st32(tO + c0, ov);
-        }
-      }
-      const float mu = m_run == -INFINITY ? 0.f : m_run;   // all masked so far: exp2(-inf) = 0
-      float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      const float2 c2 = make_float2(c, c), mu2 = make_float2(-mu, -mu);
-      {
-        uint32_t v[2][32];
-        tmem_ld32(tS, v[0]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          tmem_ld_wait();
-          if (q < 3) tmem_ld32(tS + 32 * q + 32, v[(q + 1) & 1]);
-          uint32_t(&x)[32] = v[q & 1];
-          if (masked) mask(x, q);
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float2 p = fma2(make_float2(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), c2, mu2);
-            p.x = ex2(p.x);
-            p.y = ex2(p.y);
-            ps[j & 1] = add2(ps[j & 1], p);
-            pk[j] = pack_bf16(p.x, p.y);
+          for (int i = 0; i < 32; ++i) {
+            x[i] = __uint_as_float(v0[i]);
+            x[32 + i] = __uint_as_float(v1[i]);
           }
-          tmem_st16(tS + 16 * q, pk);           // over scores that have been read
         }
+        const uint32_t mapped = mask_s[seq_v % C::kStages];
+        const int vis = bound - key0;             // visible keys of this step
+        if (__any_sync(0xffffffffu, vis < kStep) || mapped != 0xFu) {
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (j >= vis || !((mapped >> (j >> 4)) & 1u)) x[j] = -INFINITY;
+        }
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int i = 4; i < 60; i += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[i + q], x[i + 4 + q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], x[60 + q]);
+        const float mb = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+        const bool move = mb > m_run + 8.f || (m_run == -INFINITY && mb != -INFINITY);
+        float corr = 1.f;
+        if (move) {
+          corr = m_run == -INFINITY ? 0.f : ex2(m_run - mb);
+          l_run *= corr;
+          m_run = mb;
+        }
+        const float mu = m_run == -INFINITY ? 0.f : m_run;   // all masked so far: exp2(-inf) = 0
+        float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 c2 = make_float2(c, c), mu2 = make_float2(-mu, -mu);
+        uint32_t pk[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          float2 p = fma2(make_float2(x[2 * j], x[2 * j + 1]), c2, mu2);
+          p.x = ex2(p.x);
+          p.y = ex2(p.y);
+          ps[j & 1] = add2(ps[j & 1], p);
+          pk[j] = pack_bf16(p.x, p.y);
+        }
+        tmem_st32(tSe, pk);
+        l_run += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
+        if (u > 0 && __any_sync(0xffffffffu, move)) {
+          // (only the last step's product can be unfinished: the scores at hand were issued after all before it)
+          ok = __all_sync(0xffffffffu, wait(&pv_done[half], (at - 1) & 1, a.status, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t ov[32];
+            tmem_ld32(tO + c0, ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * corr);
+            tmem_st32(tO + c0, ov);
+          }
+        }
+        tmem_st_wait();
       }
-      l_run += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
       clear_tail(seq_v, key0);
-      tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&p_full[half]);
+      mbar_arrive(&p_full[2 * half + e]);
     }
     // ---------------------------------------------------------- epilogue --
     seq0 += n_places;
@@ -584,6 +590,8 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedArgs a) {
   const int tile = r / a.tile_rows, in_tile = r - tile * a.tile_rows;
   const longlong2 span = a.span[(static_cast<long long>(g) * a.B + b) * a.tiles + tile];
   const long long total = a.head[0], used = a.head[1];
+  // (a kernel that gave up waiting leaves spans unwritten: nothing is read by them)
+  if (used < 1 || used > a.workers || span.x < 0 || span.y < 1 || span.y > total || span.x > total - span.y) return;
   const int w0 = worker_of(span.x, total, used), n_part = worker_of(span.x + span.y - 1, total, used) - w0 + 1;
   if (n_part == 1) return;                              // written by its worker
   // row of piece p among the slots
