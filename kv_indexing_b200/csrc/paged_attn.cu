@@ -16,20 +16,25 @@
 //
 // A block works through the pieces of the work list (paged.cuh) that are its.
 //
-// Threads (352): warps 0-3 and 4-7 are the softmax of the two halves, one
-// thread per row; warps 8 and 10 load K and V pages by TMA into a ring of 64-key
-// tiles (boxes of one page, or of the page's part of the tile; one warp alone
-// issues boxes more slowly than HBM delivers them); one thread of warp 9 issues
-// the MMAs.
+// Threads (384): warps 0-3 and 4-7 are the softmax of the two halves, one
+// thread per row, with registers enough for a step's 128 scores (read twice from
+// tensor memory instead, or split over two threads a row, a step's softmax took
+// longer: 812 and 760 us where this takes 724); warps 8 and 10 load K and V pages by TMA into a ring of tiles
+// (boxes of one page, or of the page's part of the tile; one warp alone issues
+// boxes more slowly than HBM delivers them); one thread of warp 9 issues the
+// MMAs. Scores and O of both halves fill tensor memory. P (bf16) overwrites the
+// scores it came from and is the A operand of the second MMA. MMAs issued by one
+// thread run in order, so scores cannot overtake the product that reads their
+// buffer's last P.
 //
-// A step is 64 keys, one K and one V tile. Two scores' buffers of 64 columns and
-// O (d columns) for each half fill tensor memory: the scores of step u + 1 are
-// computed while the softmax of step u runs. P (bf16) overwrites the scores it
-// came from and is the A operand of the second MMA. MMAs issued by one thread
-// run in order, so scores cannot overtake the product that reads the buffer's
-// last P. (With steps of 128 keys and one buffer the products waited for the
-// softmax and it for them, 4100 cycles for 128 keys of 256 rows; a score product
-// of 64 keys takes 1.5 times its share, bound by shared memory, and still wins.)
+// A step is one K and one V tile.
+//   SHARED = 1: 128 keys, one buffer of scores a half. One half's products run
+//     while the other's softmax does; a half's second product starts on the
+//     first 64 keys of P. (64 keys and two buffers, as below, let the products
+//     run ahead, but a score product of 64 keys takes 1.5 times its share: its A
+//     operand, q, is read from shared memory as often as for 128.)
+//   SHARED = 0: 64 keys, two buffers a half, the scores of a half's next step
+//     computed while its softmax runs. Bound by loads, not by products.
 //
 // The running maximum only moves when a block raises it by more than 2^8 (the
 // bf16 P keeps its relative precision, sums are fp32), so O is rescaled rarely.
@@ -46,21 +51,23 @@ namespace {
 using namespace paged;
 
 constexpr int kSoft = 256;             // softmax threads
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;          // three warpgroups, for the register split
 constexpr int BN = kPagedBN;           // keys of a block of the work list
-constexpr int kStep = 64;              // keys of a step
 
 template <int D, bool SHARED>
 struct Cfg {
+  static constexpr int kStep = SHARED ? 128 : 64;      // keys of a step
   static constexpr int kChunks = D / 64;
   static constexpr int kQTile = 128 * D * 2;
   static constexpr int kQTiles = SHARED ? 2 : 1;
   static constexpr int kStage = kStep * D * 2;
-  static constexpr int kStages = D == 128 ? 10 : 20;   // at least six: half 1's next scores are issued before half 0's product
+  // SHARED = 0: at least six, since half 1's next scores are issued before half 0's product
+  static constexpr int kStages = 160 * 1024 / kStage;
   static constexpr int kOffStage = kQTiles * kQTile;
   static constexpr int kOffMask = kOffStage + kStages * kStage;
   static constexpr int kOffBars = kOffMask + ((kStages * 4 + 7) / 8) * 8;
   static constexpr int kNumBars = 2 * kStages + 15;
+  static_assert(kStages % 2 == 0 || SHARED, "K and V places");
   static constexpr int kOffWork = kOffBars + kNumBars * 8;
   static constexpr int kOffMerge = (kOffWork + 9 * static_cast<int>(sizeof(Work)) + 15) / 16 * 16;   // the block's, and the softmax warps'
   static constexpr int kMergeRow = 36;                 // floats: 32 columns, padded
@@ -68,7 +75,7 @@ struct Cfg {
   static constexpr size_t kSmem = 1024 + kOffMisc + 16;
 };
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColO = 256;   // S of half i, buffer e at 128 i + 64 e, O at 256 + D i
+constexpr uint32_t kColS = 0, kColO = 256;   // S of half i at 128 i (two buffers of 64 where a step is 64 keys), O at 256 + D i
 
 template <int D, bool SHARED>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -76,6 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const PagedArgs a) {
   using C = Cfg<D, SHARED>;
   static_assert(C::kSmem <= 227 * 1024, "shared memory budget");
+  constexpr int kStep = C::kStep;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = base;
@@ -85,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* kv_full = bars;
   uint64_t* kv_empty = bars + C::kStages;
   uint64_t* s_full = bars + 2 * C::kStages;   // [2 halves][2 buffers]
-  uint64_t* p_full = s_full + 4;              // [2][2]
+  uint64_t* p_full = s_full + 4;              // [2][2 buffers, or 64-key parts of the one]
   uint64_t* pv_done = p_full + 4;             // [2]
   uint64_t* o_full = pv_done + 2;             // [2] the piece's last product
   uint64_t* q_full = o_full + 2;
@@ -171,10 +179,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // tile of half i's step u; its K and V follow one another in the ring
   auto tile_of = [&](int i, int u) -> int { return SHARED ? u : 2 * u + i; };
 
+  // Softmax threads hold 128 scores: 208 registers each, 80 for the others (256 x 208 + 128 x 80 of the block's 384 x 168)
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   if (warp == 8 || warp == 10) {
     // ------------------------------------------------ producers (K and V) --
     const uint32_t kv = warp == 10;
-    const int box = min(kStep, 1 << a.page_shift), per = kStep / box;   // rows of a box, boxes of 64 columns
+    const int box = min(kPagedBox, 1 << a.page_shift), per = kStep / box;   // rows of a box, boxes of 64 columns
     const int n_ops = C::kChunks * per;
     const int j = lane % per, c = lane / per;
     const uint32_t groups = (1u << (box / 16)) - 1u;
@@ -223,58 +234,139 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dQ = static_cast<uint32_t>(make_sdesc(smem_u32(sQ), 16, 1024, kLayoutSW128));
       const uint32_t dK = static_cast<uint32_t>(make_sdesc(smem_u32(sStage), 16, 1024, kLayoutSW128));
       const uint32_t dV = static_cast<uint32_t>(make_sdesc(smem_u32(sStage), kStep * 128, 1024, kLayoutSW128));
-      uint32_t seq0 = 0, seg = 0, done0 = 0, done1 = 0;      // ring places, pieces, steps of the halves before this piece
+      // Places of the next K and V tile in the ring (every other stage) and their phases. Barriers are looked at before
+      // the products in front of them are issued; waiting for each when it is needed takes longer than the products.
+      struct Place {
+        int st;
+        uint32_t ph;
+        bool seen;
+      } kp{0, 0u, false}, vp{1, 0u, false};
+      auto look = [&](Place& p) { p.seen = mbar_test_wait(&kv_full[p.st], p.ph); };
+      auto take = [&](Place& p) -> bool {
+        if (!p.seen && !wait(&kv_full[p.st], p.ph, a.status, abort_flag)) return false;
+        p.seen = true;
+        tc_fence_after();
+        return true;
+      };
+      auto release = [&](Place& p) {
+        umma_commit(&kv_empty[p.st]);
+        p.seen = false;
+        if ((p.st += 2) >= C::kStages) {
+          p.st -= C::kStages;
+          p.ph ^= 1u;
+        }
+      };
+      uint32_t seg = 0, at0 = 0, at1 = 0;                    // pieces, steps of the halves before this piece
+      auto at = [&](int i, int u) -> uint32_t { return (i ? at1 : at0) + u; };
+      auto qk = [&](int i, int u) {
+        const uint32_t e = SHARED ? 0 : at(i, u) & 1, q0 = dQ + (SHARED ? i * (C::kQTile / 16) : 0);
+        const uint32_t k0 = dK + kp.st * (C::kStage / 16), d = tmem + kColS + 128 * i + kStep * e;
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            umma_f16_lo(d, q0 + c * 1024 + ks * 2, k0 + c * (kStep * 8) + ks * 2, hi, idesc_qk, (c | ks) ? 1u : 0u);
+        umma_commit(&s_full[2 * i + e]);
+      };
+      // P of half i's step u; SHARED: 64 keys of it, part e
+      auto look_p = [&](int i, int u, int e) -> bool {
+        return SHARED ? mbar_test_wait(&p_full[2 * i + e], at(i, u) & 1)
+                      : mbar_test_wait(&p_full[2 * i + (at(i, u) & 1)], (at(i, u) >> 1) & 1);
+      };
+      auto take_p = [&](int i, int u, int e, bool seen) -> bool {
+        if (!seen && !wait(&p_full[2 * i + (SHARED ? e : at(i, u) & 1)], (SHARED ? at(i, u) : at(i, u) >> 1) & 1, a.status,
+                           abort_flag))
+          return false;
+        tc_fence_after();
+        return true;
+      };
+      // the product of 64 keys of P (part e of a tile of 128)
+      auto pv = [&](int i, int u, int e) {
+        const uint32_t v0 = dV + vp.st * (C::kStage / 16) + e * 512;
+        const uint32_t p0 = tmem + kColS + 128 * i + (SHARED ? 32 * e : kStep * (at(i, u) & 1));
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          umma_f16_ts_lo(tmem + kColO + D * i, p0 + ks * 8, v0 + ks * 128, hi, idesc_pv, (u | e | ks) ? 1u : 0u);
+      };
       for (Work k = *work_s; ok && k.n > 0; next_work<kTile, BN>(a, k), ++seg) {
         const Piece p = piece_of(k);
-        const int n0 = p.n0, n1 = p.n1;
-        auto full = [&](uint32_t seq) { return wait(&kv_full[seq % C::kStages], (seq / C::kStages) & 1, a.status, abort_flag); };
-        auto qk = [&](int i, int u) -> bool {
-          const uint32_t seq = seq0 + 2 * tile_of(i, u), st = seq % C::kStages, e = ((i ? done1 : done0) + u) & 1;
-          if (!full(seq)) return false;
-          tc_fence_after();
-          const uint32_t q0 = dQ + (SHARED ? i * (C::kQTile / 16) : 0), k0 = dK + st * (C::kStage / 16);
-          const uint32_t d = tmem + kColS + 128 * i + kStep * e;
-#pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-              umma_f16_lo(d, q0 + c * 1024 + ks * 2, k0 + c * (kStep * 8) + ks * 2, hi, idesc_qk, (c | ks) ? 1u : 0u);
-          umma_commit(&s_full[2 * i + e]);
-          if (!SHARED || i == 1 || u >= n1) umma_commit(&kv_empty[st]);
-          return true;
-        };
-        auto pv = [&](int i, int u) -> bool {
-          const uint32_t seq = seq0 + 2 * tile_of(i, u) + 1, st = seq % C::kStages, at = (i ? done1 : done0) + u, e = at & 1;
-          if (!wait(&p_full[2 * i + e], (at >> 1) & 1, a.status, abort_flag) || !full(seq)) return false;
-          tc_fence_after();
-          const uint32_t v0 = dV + st * (C::kStage / 16);
-#pragma unroll
-          for (int ks = 0; ks < kStep / 16; ++ks)
-            umma_f16_ts_lo(tmem + kColO + D * i, tmem + kColS + 128 * i + kStep * e + ks * 8, v0 + ks * 128, hi, idesc_pv,
-                           (u | ks) ? 1u : 0u);
-          umma_commit(&pv_done[i]);
-          if (!SHARED || i == 1 || u >= n1) umma_commit(&kv_empty[st]);
-          if (u + 1 == (i ? n1 : n0)) umma_commit(&o_full[i]);
-          return true;
-        };
+        const int n0 = p.n0, n1 = p.n1, n = max(n0, n1);
         ok = wait(q_full, seg & 1, a.status, abort_flag);
-        if (ok && n0 > 0) ok = qk(0, 0);
-        if (ok && n1 > 0) ok = qk(1, 0);
-        const int n = max(n0, n1);
-        for (int u = 0; ok && u < n; ++u) {
-          if (u + 1 < n0) ok = qk(0, u + 1);
-          if (ok && u + 1 < n1) ok = qk(1, u + 1);
-          if (ok && u < n0) ok = pv(0, u);
-          if (ok && u < n1) ok = pv(1, u);
+        if constexpr (SHARED) {
+          if (ok && n > 0) {
+            ok = take(kp);
+            if (ok && n0 > 0) qk(0, 0);
+            if (ok && n1 > 0) qk(1, 0);
+            if (ok) release(kp);
+          }
+          for (int u = 0; ok && u < n; ++u) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int ni = i ? n1 : n0, other = i ? n0 : n1;
+              if (!ok || u >= ni) continue;
+              bool seen = look_p(i, u, 0);
+              ok = take(vp);
+              if (u + 1 < ni && !kp.seen) look(kp);
+              ok = ok && take_p(i, u, 0, seen);
+              if (!ok) break;
+              seen = look_p(i, u, 1);
+              pv(i, u, 0);
+              ok = take_p(i, u, 1, seen);
+              if (!ok) break;
+              pv(i, u, 1);
+              if (i == 1 || u >= other) release(vp);
+              if (u + 1 == ni) {
+                umma_commit(&o_full[i]);
+              } else {
+                ok = take(kp);
+                if (!ok) break;
+                qk(i, u + 1);
+                if (i == 1 || u + 1 >= other) release(kp);
+              }
+            }
+          }
+        } else {
+          // step u's scores of both halves
+          auto scores = [&](int u) -> bool {
+            if (u >= n) return true;
+            if (!take(kp)) return false;                     // (n0 = n1 or n1 + 1)
+            qk(0, u);
+            release(kp);
+            if (u < n1) {
+              if (!take(kp)) return false;
+              qk(1, u);
+              release(kp);
+            }
+            return true;
+          };
+          auto product = [&](int i, int u, int ni, bool seen) -> bool {
+            if (!take(vp) || !take_p(i, u, 0, seen)) return false;
+            pv(i, u, 0);
+            umma_commit(&pv_done[i]);
+            release(vp);
+            if (u + 1 == ni) umma_commit(&o_full[i]);
+            return true;
+          };
+          ok = ok && scores(0);
+          for (int u = 0; ok && u < n; ++u) {
+            look(vp);
+            ok = scores(u + 1);
+            if (!ok) break;
+            const bool p0 = look_p(0, u, 0);
+            look(kp);
+            ok = product(0, u, n0, p0);
+            if (ok && u < n1) ok = product(1, u, n1, false);
+          }
         }
-        seq0 += 2 * n_tiles_of(p);
-        done0 += n0;
-        done1 += n1;
+        at0 += n0;
+        at1 += n1;
       }
     }
     __syncwarp();
+  }
   } else {
     // ----------------------------------------------------------- softmax --
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int half = warp >> 2;
     const int rt = tid & 127;                   // row of the tile
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -341,84 +433,117 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m_run = -INFINITY, l_run = 0.f;       // log2 domain
 #pragma unroll 1
     for (int u = 0; u < n_steps; ++u) {
-      const uint32_t at = done + u, e = at & 1;
+      const uint32_t at = done + u, e = SHARED ? 0 : at & 1;
       const int tile = tile_of(half, u), key0 = blk0 * BN + tile * kStep;
       const uint32_t seq_v = seq0 + 2 * tile + 1;
       // the V tile's barrier also publishes the tile's mapped pages
-      ok = __all_sync(0xffffffffu, wait(&s_full[2 * half + e], (at >> 1) & 1, a.status, abort_flag) &&
+      ok = __all_sync(0xffffffffu, wait(&s_full[2 * half + e], (SHARED ? at : at >> 1) & 1, a.status, abort_flag) &&
                                        wait(&kv_full[seq_v % C::kStages], (seq_v / C::kStages) & 1, a.status, abort_flag));
       if (!ok) break;
-      if (!idle) {
-        tc_fence_after();
-        const uint32_t tSe = tS + kStep * e;
-        float x[64];
-        {
-          uint32_t v0[32], v1[32];
-          tmem_ld32(tSe, v0);
-          tmem_ld32(tSe + 32, v1);
-          tmem_ld_wait();
+      clear_tail(seq_v, key0);
+      if (idle) {
+        mbar_arrive(&p_full[2 * half + e]);
+        if (SHARED) mbar_arrive(&p_full[2 * half + 1]);
+        continue;
+      }
+      tc_fence_after();
+      const uint32_t tSe = tS + 64 * e;
+      const uint32_t mapped = mask_s[seq_v % C::kStages];
+      const int vis = bound - key0;               // visible keys of this step
+      const bool masked = __any_sync(0xffffffffu, vis < kStep) || mapped != (1u << (kStep / 16)) - 1u;
+      // scores [32 q, 32 q + 32) of the step
+      auto mask = [&](uint32_t (&v)[32], int q) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            x[i] = __uint_as_float(v0[i]);
-            x[32 + i] = __uint_as_float(v1[i]);
-          }
+        for (int j = 0; j < 32; ++j)
+          if (32 * q + j >= vis || !((mapped >> (2 * q + (j >> 4))) & 1u)) v[j] = 0xFF800000u;
+      };
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      auto largest = [&](const uint32_t (&v)[32]) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(v[j + i]), __uint_as_float(v[j + 4 + i]));
+      };
+      uint32_t v0[32], v1[32];                    // the step's first 64 scores
+      tmem_ld32(tSe, v0);
+      tmem_ld32(tSe + 32, v1);
+      tmem_ld_wait();
+      if (masked) {
+        mask(v0, 0);
+        mask(v1, 1);
+      }
+      uint32_t v2[32], v3[32];
+      if constexpr (SHARED) {
+        tmem_ld32(tSe + 64, v2);
+        tmem_ld32(tSe + 96, v3);
+      }
+      largest(v0);
+      largest(v1);
+      if constexpr (SHARED) {
+        tmem_ld_wait();
+        if (masked) {
+          mask(v2, 2);
+          mask(v3, 3);
         }
-        const uint32_t mapped = mask_s[seq_v % C::kStages];
-        const int vis = bound - key0;             // visible keys of this step
-        if (__any_sync(0xffffffffu, vis < kStep) || mapped != 0xFu) {
-#pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (j >= vis || !((mapped >> (j >> 4)) & 1u)) x[j] = -INFINITY;
-        }
-        float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-        for (int i = 4; i < 60; i += 8)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], x[i + q], x[i + 4 + q]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], x[60 + q]);
-        const float mb = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
-        const bool move = mb > m_run + 8.f || (m_run == -INFINITY && mb != -INFINITY);
+        largest(v2);
+        largest(v3);
+      }
+      const float mb = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c;
+      const bool move = mb > m_run + 8.f || (m_run == -INFINITY && mb != -INFINITY);
+      if (__any_sync(0xffffffffu, move)) {
         float corr = 1.f;
         if (move) {
           corr = m_run == -INFINITY ? 0.f : ex2(m_run - mb);
           l_run *= corr;
           m_run = mb;
         }
-        const float mu = m_run == -INFINITY ? 0.f : m_run;   // all masked so far: exp2(-inf) = 0
-        float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float2 c2 = make_float2(c, c), mu2 = make_float2(-mu, -mu);
-        uint32_t pk[32];
+        if (u > 0) {
+          // SHARED: the last product was issued before these scores, and has completed with them. Else only the last
+          // step's can be unfinished.
+          if (!SHARED) {
+            ok = __all_sync(0xffffffffu, wait(&pv_done[half], (at - 1) & 1, a.status, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+          }
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            uint32_t ov[16];
+            tmem_ld16(tO + c0, ov);
+            tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          float2 p = fma2(make_float2(x[2 * j], x[2 * j + 1]), c2, mu2);
+            for (int i = 0; i < 16; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * corr);
+            tmem_st16(tO + c0, ov);
+          }
+        }
+      }
+      const float mu = m_run == -INFINITY ? 0.f : m_run;     // all masked so far: exp2(-inf) = 0
+      float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      const float2 c2 = make_float2(c, c), mu2 = make_float2(-mu, -mu);
+      auto part = [&](const uint32_t (&v)[32], int q) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          float2 p = fma2(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), c2, mu2);
           p.x = ex2(p.x);
           p.y = ex2(p.y);
           ps[j & 1] = add2(ps[j & 1], p);
           pk[j] = pack_bf16(p.x, p.y);
         }
-        tmem_st32(tSe, pk);
-        l_run += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
-        if (u > 0 && __any_sync(0xffffffffu, move)) {
-          // (only the last step's product can be unfinished: the scores at hand were issued after all before it)
-          ok = __all_sync(0xffffffffu, wait(&pv_done[half], (at - 1) & 1, a.status, abort_flag));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 32) {
-            uint32_t ov[32];
-            tmem_ld32(tO + c0, ov);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * corr);
-            tmem_st32(tO + c0, ov);
-          }
-        }
-        tmem_st_wait();
-      }
-      clear_tail(seq_v, key0);
+        tmem_st16(tSe + 16 * q, pk);
+      };
+      part(v0, 0);
+      part(v1, 1);
+      tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&p_full[2 * half + e]);
+      if constexpr (SHARED) {
+        part(v2, 2);
+        part(v3, 3);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[2 * half + 1]);
+      }
+      l_run += (ps[0].x + ps[0].y) + (ps[1].x + ps[1].y);
     }
     // ---------------------------------------------------------- epilogue --
     seq0 += n_places;

@@ -9,6 +9,7 @@ exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -167,9 +168,15 @@ def _check(st: int):
 # ---------------------------------------------------------------------------
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -748,11 +755,20 @@ def lsa_paged_attn(q, table, seq_len, scale, *, kv=None, k=None, v=None, d_v=Non
         _out(out, "out", torch.bfloat16, shape)
     if lse is not None and not _fits(lse, torch.float32, shape[:3], cur):
         _out(lse, "lse", torch.float32, shape[:3])
-    args, size = OpArgs(paged=ctypes.pointer(pi)), ctypes.c_size_t()
-    _check(lib.lsa_workspace_size(LSA_OP_PAGED_ATTN, args, size))
-    ws = _workspace(size.value, q.device, workspace)
+    size = _paged_bytes(cur, pi.B, pi.T, pi.Hq, pi.Hkv, pi.d_qk, pi.page_size, pi.max_pages)
+    ws = _workspace(size if size else workspace_size(LSA_OP_PAGED_ATTN, paged=pi), q.device, workspace)
     _check(lib.lsa_paged_attn(pi, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.nbytes, _stream(stream)))
     return out, lse
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_bytes(device, B, T, Hq, Hkv, d, page_size, max_pages):
+    """Workspace of a paged attention call of these sizes (0: sizes that the call itself refuses)."""
+    pi = PagedAttnIn(B, T, Hq, Hkv, d, 512 if d == 576 else d, 1, page_size, max_pages, 1.0, LSA_BF16, 16, None, 16, 16, 16, 16,
+                     1 << 20, Hkv * d, 1 << 20, Hkv * d, None)
+    size = ctypes.c_size_t()
+    ok = load().lsa_workspace_size(LSA_OP_PAGED_ATTN, OpArgs(paged=ctypes.pointer(pi)), size)
+    return size.value if ok == LSA_OK else 0
 
 
 def _cache(table, ref, seq_len=None):
@@ -862,6 +878,7 @@ def lsa_pages_compact(table, ref, pools: Sequence, *, table_out=None, ref_out=No
     return table_out, ref_out, n_live
 
 
+@functools.lru_cache(maxsize=256)
 def _pages_bytes(op, n, n_pages):
     size = ctypes.c_size_t()
     _check(load().lsa_workspace_size(op, OpArgs(n=n, n_pages=n_pages), size))
