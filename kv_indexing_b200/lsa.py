@@ -563,6 +563,16 @@ def lsa_layer_group(q, w, k, seq_len, budget, layers: Sequence[dict], *, P=0, M=
 # where it is not do _need, _here and _dims work out what to raise.
 
 
+def _made(stream, make):
+    """make() on the stream that the call runs on: what it allocates must not be handed out again, nor filled,
+    in the order of another stream."""
+    if stream is None:
+        return make()
+    torch = _torch()
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        return make()
+
+
 def _fits(t, dtype, shape, cur):
     """t is a dense tensor of this type and shape on device `cur`."""
     return t is not None and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous() \
@@ -655,7 +665,7 @@ def lsa_rope(x, plan, seq_len, *, q_len=None, offset=0, inverse=False, out=None,
     if q_len is not None:
         _lengths(q_len, "q_len", B, cur)
     if out is None:
-        out = torch.zeros(shape, dtype=x.dtype, device=x.device)
+        out = _made(stream, lambda: torch.zeros(shape, dtype=x.dtype, device=x.device))
     elif not out.is_cuda or out.device.index != cur or out.dtype is not x.dtype or out.shape != shape:
         _here(out, "out", x.dtype, 4)
         _dims(out, "out", tuple(shape))
@@ -750,13 +760,15 @@ def lsa_paged_attn(q, table, seq_len, scale, *, kv=None, k=None, v=None, d_v=Non
     pi = paged_attn_in(q, table, seq_len, scale, kv=kv, k=k, v=v, d_v=d_v, kv_scale=kv_scale, q_len=q_len)
     shape, cur = (pi.B, pi.T, pi.Hq, pi.d_v), q.device.index
     if out is None:
-        out = (torch.empty if q_len is None else torch.zeros)(shape, dtype=torch.bfloat16, device=q.device)
+        make = torch.empty if q_len is None else torch.zeros
+        out = _made(stream, lambda: make(shape, dtype=torch.bfloat16, device=q.device))
     elif not _fits(out, torch.bfloat16, shape, cur):
         _out(out, "out", torch.bfloat16, shape)
     if lse is not None and not _fits(lse, torch.float32, shape[:3], cur):
         _out(lse, "lse", torch.float32, shape[:3])
     size = _paged_bytes(cur, pi.B, pi.T, pi.Hq, pi.Hkv, pi.d_qk, pi.page_size, pi.max_pages)
-    ws = _workspace(size if size else workspace_size(LSA_OP_PAGED_ATTN, paged=pi), q.device, workspace)
+    size = size if size else workspace_size(LSA_OP_PAGED_ATTN, paged=pi)
+    ws = _made(stream, lambda: _workspace(size, q.device, workspace))
     _check(lib.lsa_paged_attn(pi, out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.nbytes, _stream(stream)))
     return out, lse
 
@@ -799,12 +811,15 @@ def _pools(pools, n_pages, cur):
         shape = t.shape
         if len(shape) < 2 or shape[0] != n_pages:
             raise ValueError(f"pools[{i}] has shape {tuple(shape)}, expected ({n_pages}, ...)")
-        strides, page = t.stride(), 1
+        strides, es = t.stride(), t.element_size()
+        if n_pages > 1 and t.is_contiguous():
+            rows.append((t.data_ptr(), strides[0] * es, strides[0] * es))
+            continue
+        page = 1
         for n, step in zip(shape[:0:-1], strides[:0:-1]):
             if step != page and n != 1:
                 raise ValueError(f"pools[{i}]: a page must be contiguous")
             page *= n
-        es = t.element_size()
         rows.append((t.data_ptr(), page * es, (strides[0] if n_pages > 1 else page) * es))
     return (Pool * max(1, len(rows)))(*rows)
 
@@ -832,7 +847,7 @@ def lsa_pages_fork(table, ref, seq_len, page_size, parent, child, pools: Sequenc
     n = _list(parent, "parent", cur)
     _lengths(child, "child", n, cur)
     arr = _pools(pools, n_pages, cur)
-    ws = _workspace(_pages_bytes(LSA_OP_PAGES_FORK, n, 0), table.device, workspace)
+    ws = _made(stream, lambda: _workspace(_pages_bytes(LSA_OP_PAGES_FORK, n, 0), table.device, workspace))
     _check(load().lsa_pages_fork(table.data_ptr(), ref.data_ptr(), seq_len.data_ptr(), S, max_pages, n_pages, page_size,
                                  parent.data_ptr(), child.data_ptr(), n, arr, len(pools), _ptr(ws), _nbytes(ws),
                                  _stream(stream)))
@@ -847,7 +862,7 @@ def lsa_pages_copy(pools: Sequence, src, dst, *, workspace=None, stream=None):
     n = _list(src, "src", cur)
     _lengths(dst, "dst", n, cur)
     arr = _pools(pools, n_pages, cur)
-    ws = _workspace(_pages_bytes(LSA_OP_PAGES_COPY, n, 0), src.device, workspace)
+    ws = _made(stream, lambda: _workspace(_pages_bytes(LSA_OP_PAGES_COPY, n, 0), src.device, workspace))
     _check(load().lsa_pages_copy(arr, len(pools), n_pages, src.data_ptr(), dst.data_ptr(), n, _ptr(ws), _nbytes(ws),
                                  _stream(stream)))
 
@@ -867,11 +882,11 @@ def lsa_pages_compact(table, ref, pools: Sequence, *, table_out=None, ref_out=No
     elif not _fits(ref_out, torch.int32, (n_pages,), cur):
         _out(ref_out, "ref_out", torch.int32, (n_pages,))
     if n_live is None:
-        n_live = torch.empty(1, dtype=torch.int32, device=table.device)
+        n_live = _made(stream, lambda: torch.empty(1, dtype=torch.int32, device=table.device))
     elif not _fits(n_live, torch.int32, (1,), cur):
         _out(n_live, "n_live", torch.int32, (1,))
     arr = _pools(pools, n_pages, cur)
-    ws = _workspace(_pages_bytes(LSA_OP_PAGES_COMPACT, 0, n_pages), table.device, workspace)
+    ws = _made(stream, lambda: _workspace(_pages_bytes(LSA_OP_PAGES_COMPACT, 0, n_pages), table.device, workspace))
     _check(load().lsa_pages_compact(table.data_ptr(), ref.data_ptr(), S, max_pages, n_pages, arr, len(pools),
                                     table_out.data_ptr(), ref_out.data_ptr(), n_live.data_ptr(), _ptr(ws), _nbytes(ws),
                                     _stream(stream)))

@@ -216,6 +216,44 @@ def test_captured_call_follows_new_lengths(d, kind, T):
     assert L.lsa_device_status() == 0
 
 
+def test_stream_argument_orders_what_the_call_allocates():
+    """Outputs and workspaces of a call on `stream` belong to that stream: the current one is busy for a while, and
+    allocates right after the call."""
+    d, st = 128, torch.cuda.Stream()
+    c = Cache([5000, 130], 32, (2, d))
+    pools = [c.pool()[0] for _ in range(2)]
+    q = torch.randn(2, 3, 8, d, generator=c.gen, device="cuda").to(torch.bfloat16)
+    ql, plan = ints([3, 2]), L.lsa_rope_plan(64, 10000.0)
+    want, _ = L.lsa_paged_attn(q, c.table, c.seq_len, 0.1, k=pools[0], v=pools[1], q_len=ql)
+    turned = L.lsa_rope(q, plan, c.seq_len, q_len=ql)
+    torch.cuda.synchronize()
+    for handle in (st, st.cuda_stream):
+        torch.cuda._sleep(50_000_000)                       # a quarter of the wait limit at most, on the current stream
+        got, _ = L.lsa_paged_attn(q, c.table, c.seq_len, 0.1, k=pools[0], v=pools[1], q_len=ql, stream=handle)
+        rot = L.lsa_rope(q, plan, c.seq_len, q_len=ql, stream=handle)
+        st.synchronize()
+        assert torch.equal(got, want) and torch.equal(rot, turned)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(rot, turned)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, with workspaces of their own."""
+    sets = []
+    for seed, d, kind in ((1, 128, "bf16"), (2, 576, "bf16"), (3, 576, "e4m3")):
+        c, q, pools, out, lse = run([3000, 40], [5, 5], 8, 1, d, 32, kind=kind, seed=seed)
+        sets.append((c, q, pools, out, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for c, q, pools, out, st in sets:
+            with torch.cuda.stream(st):
+                got.append((call(c, q, 1 / math.sqrt(q.shape[-1]), pools, [5, 5])[0], out))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in got)
+    assert L.lsa_device_status() == 0
+
+
 # ------------------------------------------------------------------ together
 class Server:
     """A decoder layer's paged cache as a serving loop keeps it: latent rows (576 columns, the last 64 rotated)."""
