@@ -236,7 +236,9 @@ cudaError_t launch_fork(const PageArgs& a, const int* parent, const int* child, 
                         const Pools& pools, int rows, cudaStream_t stream);
 cudaError_t launch_copy_plan(int n_pages, const int* src, const int* dst, int n, int* ok, int* status,
                              cudaStream_t stream);
-cudaError_t launch_copy(const Pools& pools, const int* src, const int* dst, const int* ok, int n, cudaStream_t stream);
+constexpr int kCopyNoPlan = 1024;    // up to so many pairs the copying blocks check them themselves (ok null)
+cudaError_t launch_copy(const Pools& pools, const int* src, const int* dst, const int* ok, int n, int n_pages, int* status,
+                        cudaStream_t stream);
 // ws: counters [2] (n_live, moves), then src [n_pages], dst [n_pages], map [n_pages]
 cudaError_t launch_compact_plan(const int* ref, int n_pages, int* ref_out, int* n_live, int* ws, cudaStream_t stream);
 cudaError_t launch_compact(const int* table, int S, int max_pages, int n_pages, int* table_out, const int* ws,

@@ -334,12 +334,28 @@ __global__ void __launch_bounds__(kPlan) copy_plan_kernel(int n_pages, const int
   }
 }
 
+// ok null: every block looks through the list for its own pair (few pairs: less than a launch for a plan).
 __global__ void __launch_bounds__(kMove) copy_kernel(const int* __restrict__ src, const int* __restrict__ dst,
-                                                     const int* __restrict__ ok, const __grid_constant__ Pools pools) {
+                                                     const int* __restrict__ ok, int n, int n_pages, int* status,
+                                                     const __grid_constant__ Pools pools) {
   pdl_wait();
   pdl_trigger();
-  if (!ok[blockIdx.x]) return;
-  move_piece(pools, blockIdx.y, src[blockIdx.x], dst[blockIdx.x]);
+  const int me = blockIdx.x, s = src[me], d = dst[me];
+  if (ok) {
+    if (!ok[me]) return;
+  } else {
+    auto inside = [&](int p) { return p >= 0 && p < n_pages; };
+    bool refused = !inside(s) || !inside(d);
+    for (int i = threadIdx.x; i < n && !refused; i += kMove) {
+      const int si = src[i], di = dst[i];
+      refused = inside(si) && inside(di) && ((di == d && i != me) || si == d);
+    }
+    if (__syncthreads_or(refused)) {
+      if (threadIdx.x == 0) record_bad_page(status);
+      return;
+    }
+  }
+  move_piece(pools, blockIdx.y, s, d);
 }
 
 // ------------------------------------------------------------------ compact --
@@ -511,9 +527,9 @@ cudaError_t launch_copy_plan(int n_pages, const int* src, const int* dst, int n,
                      static_cast<size_t>((n_pages + 31) / 32) * 8, stream, n_pages, src, dst, n, ok, status);
 }
 
-cudaError_t launch_copy(const Pools& pools, const int* src, const int* dst, const int* ok, int n,
+cudaError_t launch_copy(const Pools& pools, const int* src, const int* dst, const int* ok, int n, int n_pages, int* status,
                         cudaStream_t stream) {
-  void* args[] = {&src, &dst, &ok, const_cast<Pools*>(&pools)};
+  void* args[] = {&src, &dst, &ok, &n, &n_pages, &status, const_cast<Pools*>(&pools)};
   return launch_pdl(reinterpret_cast<const void*>(&copy_kernel), dim3(n, pools.first[pools.n]), dim3(kMove), 0, stream,
                     args);
 }

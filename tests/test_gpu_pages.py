@@ -236,7 +236,7 @@ def test_no_pages_left():
     d.check()
 
 
-@pytest.mark.parametrize("n_pages,n", [(2, 1), (33, 5), (2000, 700), (1 << 19, 2000)])
+@pytest.mark.parametrize("n_pages,n", [(2, 1), (33, 5), (2000, 700), (2100, 1025), (1 << 19, 2000)])
 def test_copy(n_pages, n):
     g = torch.Generator(device="cuda").manual_seed(n)
     perm = torch.randperm(n_pages, generator=g, device="cuda").to(torch.int32)
@@ -252,13 +252,18 @@ def test_copy(n_pages, n):
     assert all(torch.equal(a, b) for a, b in zip(pools, want))
 
 
-def test_copy_refuses_pairs_that_depend_on_order():
-    pool = torch.arange(20 * 16, device="cuda", dtype=torch.float32).reshape(20, 16)
+@pytest.mark.parametrize("extra", [0, 1100])
+def test_copy_refuses_pairs_that_depend_on_order(extra):
+    """`extra` further pairs, all fine: beyond 1024 the list is checked by a kernel of its own."""
+    pool = torch.arange((20 + 2 * extra) * 16, device="cuda", dtype=torch.float32).reshape(-1, 16)
     want = pool.clone()
     want[9] = want[1]
+    want[20 + extra:] = want[20:20 + extra].clone()
     #        fine, out of range, the same dst twice, dst read by another, onto itself
     src, dst = [1, 20, 2, 3, 4, 5, 6, 7], [9, 3, -1, 10, 10, 6, 11, 7]
     want[11] = want[6]
+    src[1] = 20 + 2 * extra
+    src, dst = src + list(range(20, 20 + extra)), dst + list(range(20 + extra, 20 + 2 * extra))
     L.lsa_pages_copy([pool], ints(src), ints(dst))
     with pytest.raises(L.LsaError, match="refused"):
         L.lsa_device_status()

@@ -185,7 +185,7 @@ def test_upkeep_refusals():
         assert fork(2, 256, 4096, (L.Pool * 1)(L.Pool(*bad))) == code, bad
     assert fork(2, 256, 4096, None) == INVALID
     assert lib.lsa_pages_copy(pools, 1, 40, x, None, 3, 256, 4096, None) == INVALID
-    assert lib.lsa_pages_copy(pools, 1, 40, x, x, 3, 256, 0, None) == WORKSPACE
+    assert lib.lsa_pages_copy(pools, 1, 40, x, x, 1025, 256, 0, None) == WORKSPACE
     assert lib.lsa_pages_copy(pools, 1, 0, x, x, 3, 256, 4096, None) == INVALID
     n = L.workspace_size(L.LSA_OP_PAGES_COMPACT, n_pages=40)
     comp = lambda tout, rout, nb: lib.lsa_pages_compact(t, r, 4, 8, 40, pools, 1, tout, rout, None, 256, nb, None)  # noqa: E731
