@@ -269,7 +269,8 @@ struct PagedArgs {
   const float* k_scale;   // e4m3: [n_pages, page_size]
   int* status;
 };
-// K and V as (columns, slot, page) with boxes of 64 columns (e4m3: 128) x box rows x 1 page.
+// K and V as (columns, slot, page) with boxes of 64 columns (e4m3: 128) x box rows x 1 page; latent rows: v is q as
+// (columns, row) with boxes of 64 x 64.
 struct PagedMaps {
   CUtensorMap k, v;
 };

@@ -94,9 +94,17 @@ __device__ __forceinline__ Work plan_work(const PagedArgs& a, int w, int workers
   }
   Work k{};
   if (w >= used) return k;
-  const long long s = total * w / used;
-  k.left = total * (w + 1) / used - s;
-  k.g = static_cast<int>(s / sum);
+  long long s;
+  if (total <= 0x00FFFFFFll) {              // 32-bit divisions: a third of the time (workers are at most 160)
+    const uint32_t t = static_cast<uint32_t>(total), u = static_cast<uint32_t>(used);
+    s = t * static_cast<uint32_t>(w) / u;
+    k.left = t * static_cast<uint32_t>(w + 1) / u - s;
+    k.g = static_cast<int>(static_cast<uint32_t>(s) / static_cast<uint32_t>(sum));
+  } else {
+    s = total * w / used;
+    k.left = total * (w + 1) / used - s;
+    k.g = static_cast<int>(s / sum);
+  }
   long long at = k.g * sum;                 // the list position of tile i0
   for (int i0 = 0;; i0 += 32) {
     const int n = i0 + lane < n_bt ? blocks_of<ROWS, BN>(a, i0 + lane) : 0;
@@ -141,6 +149,8 @@ __device__ __forceinline__ void next_work(const PagedArgs& a, Work& k) {
 
 // The worker that has position x of a list of `total`.
 __device__ __forceinline__ int worker_of(long long x, long long total, long long used) {
+  if (total <= 0x00FFFFFFll)
+    return static_cast<int>((static_cast<uint32_t>(x + 1) * static_cast<uint32_t>(used) - 1u) / static_cast<uint32_t>(total));
   return static_cast<int>(((x + 1) * used - 1) / total);
 }
 

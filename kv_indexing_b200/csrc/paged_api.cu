@@ -87,6 +87,19 @@ lsa_status_t page_map(CUtensorMap* m, const void* base, bool e4m3, int cols, int
   return LSA_OK;
 }
 
+// q [rows, 576] bf16, boxes of 64 columns x 64 rows.
+lsa_status_t query_map(CUtensorMap* m, const void* base, uint64_t rows) {
+  auto fn = encoder();
+  if (!fn) return set_error(LSA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t dims[2] = {576, rows}, strides[1] = {576 * 2};
+  cuuint32_t box[2] = {64, 64}, estr[2] = {1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(LSA_ERR_CUDA, "cuTensorMapEncodeTiled (q) failed (%d)", static_cast<int>(r));
+  return LSA_OK;
+}
+
 // --------------------------------------------------------- paged attention --
 bool is_mla(const lsa_paged_attn_in_t* in) { return in->d_qk == 576; }
 
@@ -411,6 +424,7 @@ lsa_status_t lsa_paged_attn(const lsa_paged_attn_in_t* in, void* out, float* lse
     if ((s = page_map(&m.k, in->k, e4m3, 576, in->page_size, in->n_pages, in->k_row_stride, in->k_page_stride,
                       std::min(in->page_size, kPagedBox))) != LSA_OK)
       return s;
+    if ((s = query_map(&m.v, in->q, static_cast<uint64_t>(in->B) * in->T * in->Hq)) != LSA_OK) return s;
     s = cuda_check(launch_paged_mla(m, a, e4m3, st), "paged latent attention launch");
   } else {
     const int box = std::min(in->page_size, kPagedBox);

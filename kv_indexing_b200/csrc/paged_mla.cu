@@ -74,8 +74,8 @@ struct Lay {
   static constexpr int kOffSwap = kOffRaw + kRaw * kChunk;       // [2][128] what a row's two threads tell each other
   static constexpr int kOffScale = kOffSwap + 2 * 128 * 4;       // e4m3: [4 warps][64] scales of the block's keys
   static constexpr int kOffBars = kOffScale + 4 * 64 * 4;
-  // full, empty, raw_full, raw_empty, s_full, s_free, p_full[2], pv_done, o_full, q_full, tail[4], swap[2]
-  static constexpr int kNumBars = 2 * kSlots + 2 * kRaw + 13;
+  // full, empty, raw_full, raw_empty, s_full, s_free, p_full[2], pv_done, o_full, q_full, tail[4], swap[2], q_tma, p_idle
+  static constexpr int kNumBars = 2 * kSlots + 2 * kRaw + 15;
   static constexpr int kOffWork = kOffBars + kNumBars * 8;
   static constexpr int kOffMisc = kOffWork + static_cast<int>(sizeof(Work));
   static constexpr size_t kSmem = 1024 + kOffMisc + 16;
@@ -98,7 +98,7 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t four) {
 
 template <bool KV8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 1)
-    paged_mla_kernel(const __grid_constant__ CUtensorMap tm_k, const PagedArgs a) {
+    paged_mla_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const PagedArgs a) {
   using Y = Lay<KV8>;
   constexpr int kSlots = Y::kSlots, kRaw = Y::kRaw, kMmaWarp = Y::kMmaWarp;
   extern __shared__ uint8_t smem_raw[];
@@ -119,6 +119,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
   uint64_t* q_full = o_full + 1;       // CTA 0
   uint64_t* tail = q_full + 1;         // [4] a slot that is cleared in part before it counts, by loading warp
   uint64_t* swap = tail + 4;           // [2] warps w and w + 2 have stored theirs
+  uint64_t* q_tma = swap + 2;          // q's columns in shared memory
+  uint64_t* p_idle = q_tma + 1;        // the softmax warps are through with P's buffers
   Work* work_s = reinterpret_cast<Work*>(base + Y::kOffWork);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + Y::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -145,6 +147,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
     mbar_init(q_full, 8);
     for (int i = 0; i < 4; ++i) mbar_init(&tail[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&swap[i], 2);
+    mbar_init(q_tma, 1);
+    mbar_init(p_idle, 4);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -476,28 +480,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
       const int* trow = a.table + static_cast<long long>(b) * a.max_pages;
       const long long q0 = static_cast<long long>(b) * a.T * a.Hq + row0;   // the CTA's first row of q and out
       {
+        // q's columns: [0, 256) by TMA into P's buffers and from there into tensor memory, [256, 384) into tensor memory
+        // by loads, [384, 576) by TMA where the MMA reads them. (All by loads of each thread's row: 13000 cycles.) Rows
+        // behind the sequence's last are whatever lies there; no row meets another.
+        if (warp == 0) {
+          if (seg > 0) ok = __all_sync(0xffffffffu, wait(p_idle, (seg - 1) & 1, a.status, abort_flag));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(q_tma, (9 - kTmemChunks + 4) * kChunk);
+          __syncwarp();
+          if (lane < 9 - kTmemChunks + 4) {
+            const int ch = lane < 4 ? lane : kTmemChunks + lane - 4;
+            tma_load_2d(lane < 4 ? sP + lane * kChunk : sQ + (lane - 4) * kChunk, &tm_q, q_tma, ch * 64, static_cast<int>(q0));
+          }
+        }
         const bool mine = row0 + r < rows;
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (q0 + r) * 576);
-#pragma unroll 2
-        for (int ch = 0; ch < kTmemChunks; ++ch) {     // two bf16 per column, ascending; both threads of a row
-          uint32_t v[32];
+        uint32_t v[2][32];
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch)               // two bf16 per column, ascending; both threads of a row
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const uint4 w = mine ? __ldg(src + ch * 8 + u) : make_uint4(0u, 0u, 0u, 0u);
-            v[4 * u] = w.x;
-            v[4 * u + 1] = w.y;
-            v[4 * u + 2] = w.z;
-            v[4 * u + 3] = w.w;
+            const uint4 w = mine ? __ldg(src + (4 + ch) * 8 + u) : make_uint4(0u, 0u, 0u, 0u);
+            v[ch][4 * u] = w.x;
+            v[ch][4 * u + 1] = w.y;
+            v[ch][4 * u + 2] = w.z;
+            v[ch][4 * u + 3] = w.w;
           }
-          tmem_st32(tQ + lane_base + ch * 32, v);
-        }
+        tmem_st32(tQ + lane_base + 4 * 32, v[0]);
+        tmem_st32(tQ + lane_base + 5 * 32, v[1]);
+        ok = __all_sync(0xffffffffu, wait(q_tma, seg & 1, a.status, abort_flag));
+        if (!ok) break;
 #pragma unroll
-        for (int u = h; u < (9 - kTmemChunks) * 8; u += 2) {
-          const uint4 w = mine ? __ldg(src + kTmemChunks * 8 + u) : make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4*>(sQ + (u >> 3) * kChunk + r * 128 + (((u & 7) ^ (r & 7)) << 4)) = w;
+        for (int ch = 0; ch < 4; ++ch) {
+          uint32_t x[32];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const uint4 w = *reinterpret_cast<const uint4*>(sP + ch * kChunk + r * 128 + ((u ^ (r & 7)) << 4));
+            x[4 * u] = w.x;
+            x[4 * u + 1] = w.y;
+            x[4 * u + 2] = w.z;
+            x[4 * u + 3] = w.w;
+          }
+          tmem_st32(tQ + lane_base + ch * 32, x);
         }
         tmem_st_wait();
-        fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_at(q_full0);
@@ -659,43 +685,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
       const int slot = 2 * worker + (k.blk0 == 0);
       const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
       const int wrow = (warp & 1) * 32;            // the warp's first row
-      float* tile_s = reinterpret_cast<float*>(sP) + warp * 32 * 36;   // [32 rows][36]
+      // [32 rows][64 floats], 16-byte units XOR-swizzled by the row
+      float4* tile_s = reinterpret_cast<float4*>(sP + warp * 8192);
 #pragma unroll 1
-      for (int q = 0; q < 8; ++q) {
-        uint32_t ov[32];
-        tmem_ld32(tO + lane_base + q * 32, ov);
+      for (int q = 0; q < 4; ++q) {
+        const int col = (q >> 1) * 256 + h * 128 + (q & 1) * 64;
+        uint32_t ov[2][32];
+        tmem_ld32(tO + lane_base + q * 64, ov[0]);
+        tmem_ld32(tO + lane_base + q * 64 + 32, ov[1]);
         tmem_ld_wait();
-        float4* mine4 = reinterpret_cast<float4*>(tile_s + lane * 36);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int u = 0; u < 16; ++u) {
+          const uint32_t* o = ov[u >> 3] + 4 * (u & 7);
           float4 w = make_float4(0.f, 0.f, 0.f, 0.f);      // a row without keys is 0
           if (l_run > 0.f)
-            w = make_float4(__uint_as_float(ov[4 * i]) * inv, __uint_as_float(ov[4 * i + 1]) * inv,
-                            __uint_as_float(ov[4 * i + 2]) * inv, __uint_as_float(ov[4 * i + 3]) * inv);
-          mine4[i] = w;
+            w = make_float4(__uint_as_float(o[0]) * inv, __uint_as_float(o[1]) * inv, __uint_as_float(o[2]) * inv,
+                            __uint_as_float(o[3]) * inv);
+          tile_s[lane * 16 + (u ^ (lane & 15))] = w;
         }
         __syncwarp();
-        const int col = (q >> 2) * 256 + h * 128 + (q & 3) * 32;
         if (whole) {
-          // 8 rows per instruction, 64 bytes (32 bf16) per row
+          // 4 rows per instruction, 128 bytes (64 bf16) per row
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = i * 8 + (lane >> 2), sg = lane & 3;
-            const float4* sp = reinterpret_cast<const float4*>(tile_s + rr * 36 + sg * 8);
-            const float4 v0 = sp[0], v1 = sp[1];
+          for (int i = 0; i < 8; ++i) {
+            const int rr = i * 4 + (lane >> 3), u = 2 * (lane & 7);
+            const float4 v0 = tile_s[rr * 16 + (u ^ (rr & 15))], v1 = tile_s[rr * 16 + ((u + 1) ^ (rr & 15))];
             if (row0 + wrow + rr < rows)
-              *reinterpret_cast<uint4*>(a.out + (q0 + wrow + rr) * 512 + col + sg * 8) =
+              *reinterpret_cast<uint4*>(a.out + (q0 + wrow + rr) * 512 + col + 4 * u) =
                   make_uint4(pack_bf16(v0.x, v0.y), pack_bf16(v0.z, v0.w), pack_bf16(v1.x, v1.y), pack_bf16(v1.z, v1.w));
           }
         } else {
-          // 4 rows per instruction, 128 bytes (32 fp32) per row
+          // 2 rows per instruction, 256 bytes (64 fp32) per row
+          float* to = a.part_o + (static_cast<long long>(slot) * kRows + rank * 64 + wrow) * 512 + col;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int rr = i * 4 + (lane >> 3), sg = lane & 7;
-            const float4 v0 = *reinterpret_cast<const float4*>(tile_s + rr * 36 + sg * 4);
-            if (row0 + wrow + rr < rows)
-              *reinterpret_cast<float4*>(a.part_o + (static_cast<long long>(slot) * kRows + rank * 64 + wrow + rr) * 512 + col +
-                                         sg * 4) = v0;
+          for (int i = 0; i < 16; ++i) {
+            const int rr = i * 2 + (lane >> 4), u = lane & 15;
+            const float4 v0 = tile_s[rr * 16 + (u ^ (rr & 15))];
+            if (row0 + wrow + rr < rows) *reinterpret_cast<float4*>(to + rr * 512 + 4 * u) = v0;
           }
         }
         __syncwarp();
@@ -709,6 +735,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
         }
       }
       if (tid == 0 && rank == 0 && k.blk0 == 0) a.span[k.bt] = make_longlong2(k.begin, k.all);
+      fence_proxy_async_smem();                    // the next piece's q comes into P's buffers by TMA
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_idle);
     }
   }
 
@@ -729,7 +758,7 @@ static cudaError_t launch_mla_t(const PagedMaps& m, const PagedArgs& a, cudaStre
   const void* fn = reinterpret_cast<const void*>(&paged_mla_kernel<KV8>);
   const cudaError_t e = set_max_smem(fn, Lay<KV8>::kSmem);
   if (e != cudaSuccess) return e;
-  void* args[] = {const_cast<CUtensorMap*>(&m.k), const_cast<PagedArgs*>(&a)};
+  void* args[] = {const_cast<CUtensorMap*>(&m.k), const_cast<CUtensorMap*>(&m.v), const_cast<PagedArgs*>(&a)};
   return launch_pdl(fn, dim3(2 * a.workers), dim3(Lay<KV8>::kThreads), Lay<KV8>::kSmem, stream, args);
 }
 
