@@ -35,8 +35,17 @@
 // the layout of the pair's accumulator); warps 4-7 load every fourth slot each
 // (TMA boxes of one page, or of the page's part of 64 keys; one warp alone issues
 // boxes at 7 TB/s over the GPU, two at 13, four at 19); the last warp of CTA 0
-// issues the MMAs. e4m3: warps 4-5 load raw codes and warps 6-13 convert them
-// (codes -> bf16, exact); a key's scale multiplies its score and its P.
+// issues the MMAs.
+//
+// e4m3: warps 4-5 load raw codes and warps 6-13 convert them for the products,
+// which take fp16 here: a code is an fp16 value, exactly, by one instruction per
+// pair (to bf16 it takes four, and they bound the kernel: 401 us where this takes
+// 379). q goes to fp16 times a power of two per row that brings its largest
+// column to [2^14, 2^15): exact but for columns 2^28 below that, by 2^-40 of it.
+// A key's scale multiplies its score and its P. P times the scale, with p at most
+// 2^8, is brought below 2^15 by a power of two that follows the largest scale so
+// far and rounded to fp16: to 2^-11, or by 2^-32 of the largest P where it is
+// below 2^-29 of it. All three powers of two are taken back in fp32.
 //
 // The running maximum moves only when a block raises it by more than 2^8 (P in
 // bf16 keeps its relative precision, sums are fp32), so O is rescaled rarely.
@@ -72,8 +81,8 @@ struct Lay {
   static constexpr int kSlots = KV8 ? 6 : 10, kRaw = KV8 ? 8 : 0;
   static constexpr int kOffRaw = kOffRing + kSlots * kSlot;
   static constexpr int kOffSwap = kOffRaw + kRaw * kChunk;       // [2][128] what a row's two threads tell each other
-  static constexpr int kOffScale = kOffSwap + 2 * 128 * 4;       // e4m3: [4 warps][64] scales of the block's keys
-  static constexpr int kOffBars = kOffScale + 4 * 64 * 4;
+  static constexpr int kOffScale = kOffSwap + 2 * 128 * 4;       // e4m3: [4 warps][2][64] what multiplies scores and P
+  static constexpr int kOffBars = kOffScale + (KV8 ? 2 : 0) * 4 * 64 * 4;
   // full, empty, raw_full, raw_empty, s_full, s_free, p_full[2], pv_done, o_full, q_full, tail[4], swap[2], q_tma, p_idle
   static constexpr int kNumBars = 2 * kSlots + 2 * kRaw + 15;
   static constexpr int kOffWork = kOffBars + kNumBars * 8;
@@ -85,15 +94,20 @@ struct Lay {
                     kSmem <= 227 * 1024, "shared memory layout");
 };
 
-// Two of four e4m3 codes (the lower or the upper pair) -> a bf16 pair, exact.
-// (Moving the bits and a multiplication by 2^120 takes one instruction more per
-// pair: 452 us where this takes 411.)
+// Two of four e4m3 codes (the lower or the upper pair) -> an fp16 pair, exact.
 template <int HIGH>
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t four) {
+__device__ __forceinline__ uint32_t codes_to_f16(uint32_t four) {
   uint32_t h2;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(HIGH ? four >> 16 : four)));
-  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-  return pack_bf16(f.x, f.y);
+  return h2;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_bf16(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
 template <bool KV8>
@@ -174,8 +188,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
     // issued: waiting for each in turn, with the products in between, took
     // longer (3700 cycles a block) than the products themselves.
     if (rank == 0 && elect_one()) {
-      const uint32_t idesc_qk = make_idesc(1, 1, 128, BN, 0, 0);
-      const uint32_t idesc_pv = make_idesc(1, 1, 128, 256, 0, 1);
+      constexpr uint32_t kType = KV8 ? 0 : 1;     // fp16, bf16
+      const uint32_t idesc_qk = make_idesc(kType, kType, 128, BN, 0, 0);
+      const uint32_t idesc_pv = make_idesc(kType, kType, 128, 256, 0, 1);
       const uint32_t hi = static_cast<uint32_t>(make_sdesc(0, 16, 1024, kLayoutSW128) >> 32);
       const uint32_t dQ = static_cast<uint32_t>(make_sdesc(smem_u32(sQ), 16, 1024, kLayoutSW128));
       const uint32_t dP = static_cast<uint32_t>(make_sdesc(smem_u32(sP), 16, 1024, kLayoutSW128));
@@ -393,7 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
           }
         }
       } else {
-        // --------------------------- e4m3: codes -> bf16, into the ring --
+        // --------------------------- e4m3: codes -> fp16, into the ring --
         // Two groups of four warps take alternate slots, one code path for all of
         // them (a path for K and one for V, with their codes in registers, ran at
         // a sixth of an instruction a cycle). A lane converts 8 codes at a time;
@@ -438,7 +453,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
                 uint2 e = *reinterpret_cast<const uint2*>(src + r * 128 + c * 64 + unit * 8);
                 if (r >= rows) e = make_uint2(0u, 0u);           // past seq_len, whatever the page holds
                 *reinterpret_cast<uint4*>(dst + c * kChunk + r * 128 + ((unit ^ (r & 7)) << 4)) =
-                    make_uint4(codes_to_bf16<0>(e.x), codes_to_bf16<1>(e.x), codes_to_bf16<0>(e.y), codes_to_bf16<1>(e.y));
+                    make_uint4(codes_to_f16<0>(e.x), codes_to_f16<1>(e.x), codes_to_f16<0>(e.y), codes_to_f16<1>(e.y));
               }
             }
             fence_proxy_async_smem();
@@ -458,8 +473,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t p_full0 = mapa_shared(smem_u32(p_full), 0), q_full0 = mapa_shared(smem_u32(q_full), 0);
     const uint32_t s_free0 = mapa_shared(smem_u32(s_free), 0);
-    float* scale_s = reinterpret_cast<float*>(base + Y::kOffScale) + warp * 64;
-    const float c = a.scale_log2;
+    float* scale_s = reinterpret_cast<float*>(base + Y::kOffScale) + warp * 128;   // [2][64]
     uint32_t jb = 0, seg = 0, n_swap = 0;
     // Tells the row's other thread v and returns its value (through alternate buffers: a value is read before the
     // partner can get to the exchange after the next).
@@ -479,7 +493,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
       const int rows = L.n_new * a.Hq;
       const int* trow = a.table + static_cast<long long>(b) * a.max_pages;
       const long long q0 = static_cast<long long>(b) * a.T * a.Hq + row0;   // the CTA's first row of q and out
+      float c;                                     // score -> log2 domain
       {
+        c = a.scale_log2;
         // q's columns: [0, 256) by TMA into P's buffers and from there into tensor memory, [256, 384) into tensor memory
         // by loads, [384, 576) by TMA where the MMA reads them. (All by loads of each thread's row: 13000 cycles.) Rows
         // behind the sequence's last are whatever lies there; no row meets another.
@@ -506,20 +522,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
             v[ch][4 * u + 2] = w.z;
             v[ch][4 * u + 3] = w.w;
           }
-        tmem_st32(tQ + lane_base + 4 * 32, v[0]);
-        tmem_st32(tQ + lane_base + 5 * 32, v[1]);
+        if constexpr (!KV8) {
+          tmem_st32(tQ + lane_base + 4 * 32, v[0]);
+          tmem_st32(tQ + lane_base + 5 * 32, v[1]);
+        }
         ok = __all_sync(0xffffffffu, wait(q_tma, seg & 1, a.status, abort_flag));
         if (!ok) break;
+        auto unit = [&](uint8_t* chunk, int u) -> uint4* {
+          return reinterpret_cast<uint4*>(chunk + r * 128 + ((u ^ (r & 7)) << 4));
+        };
+        float up = 1.f;                              // e4m3: the row's power of two
+        if constexpr (KV8) {
+          float top = 0.f;
+          auto see = [&](uint32_t w) {
+            const float2 f = unpack_bf16(w);
+            top = max3(top, fabsf(f.x), fabsf(f.y));
+          };
 #pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            see(v[0][i]);
+            see(v[1][i]);
+          }
+#pragma unroll 4
+          for (int i = h; i < (9 - kTmemChunks + 4) * 8; i += 2) {   // the row's threads share the rest
+            const uint4 w = *unit((i < 32 ? sP : sQ - 4 * kChunk) + (i >> 3) * kChunk, i & 7);
+            see(w.x);
+            see(w.y);
+            see(w.z);
+            see(w.w);
+          }
+          float other;
+          ok = exchange(top, &other);
+          if (!ok) break;
+          const int e = 14 + 127 - static_cast<int>(__float_as_uint(fmaxf(top, other)) >> 23);
+          const int pow = max(-100, min(100, e));
+          up = __uint_as_float(static_cast<uint32_t>(pow + 127) << 23);
+          c = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - pow) << 23);
+        }
+        auto to_type = [&](uint32_t w) -> uint32_t {
+          if constexpr (!KV8) return w;
+          const float2 f = unpack_bf16(w);
+          return pack_f16(f.x * up, f.y * up);
+        };
+        if constexpr (KV8) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            v[0][i] = to_type(v[0][i]);
+            v[1][i] = to_type(v[1][i]);
+          }
+          tmem_st32(tQ + lane_base + 4 * 32, v[0]);
+          tmem_st32(tQ + lane_base + 5 * 32, v[1]);
+          for (int i = h; i < (9 - kTmemChunks) * 8; i += 2) {
+            uint4* at = unit(sQ + (i >> 3) * kChunk, i & 7);
+            const uint4 w = *at;
+            *at = make_uint4(to_type(w.x), to_type(w.y), to_type(w.z), to_type(w.w));
+          }
+          fence_proxy_async_smem();
+        }
+#pragma unroll 1
         for (int ch = 0; ch < 4; ++ch) {
           uint32_t x[32];
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const uint4 w = *reinterpret_cast<const uint4*>(sP + ch * kChunk + r * 128 + ((u ^ (r & 7)) << 4));
-            x[4 * u] = w.x;
-            x[4 * u + 1] = w.y;
-            x[4 * u + 2] = w.z;
-            x[4 * u + 3] = w.w;
+            const uint4 w = *unit(sP + ch * kChunk, u);
+            x[4 * u] = to_type(w.x);
+            x[4 * u + 1] = to_type(w.y);
+            x[4 * u + 2] = to_type(w.z);
+            x[4 * u + 3] = to_type(w.w);
           }
           tmem_st32(tQ + lane_base + ch * 32, x);
         }
@@ -535,40 +604,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
         const int tok = (k.blk0 + j) * BN + lane * 16;
         return lane < 8 && j < k.n && tok < L.len ? __ldg(trow + (tok >> a.page_shift)) : kNoPage;
       };
-      // e4m3: the scale of key 64 h + i of block j (0 where there is none)
+      // e4m3: this lane's four of the block's scales, keys 64 h + lane + {0, 32} and those of the other half (0 where
+      // there is none)
+      auto key_at = [&](int j, int i) -> int { return (k.blk0 + j) * BN + (64 * h ^ (i & 2) * 32) + lane + (i & 1) * 32; };
       auto page_at = [&](int j, int i) -> int {
-        const int tok = (k.blk0 + j) * BN + 64 * h + i;
+        const int tok = key_at(j, i);
         return j < k.n && tok < L.len ? __ldg(trow + (tok >> a.page_shift)) : kNoPage;
       };
       auto scale_at = [&](int j, int i, int page) -> float {
-        const int tok = (k.blk0 + j) * BN + 64 * h + i;
-        return page < 0 || page >= a.n_pages ? 0.f
-                                             : __ldg(a.k_scale + (static_cast<long long>(page) << a.page_shift) + (tok & ((1 << a.page_shift) - 1)));
+        if (page < 0 || page >= a.n_pages) return 0.f;
+        return __ldg(a.k_scale + (static_cast<long long>(page) << a.page_shift) + (key_at(j, i) & ((1 << a.page_shift) - 1)));
       };
       int entry = entry_of(0);
-      float sc0 = 0.f, sc1 = 0.f;
-      int pg0 = -1, pg1 = -1;
+      float sc[4];
+      int pg[4];
       if constexpr (KV8) {
-        sc0 = scale_at(0, lane, page_at(0, lane));
-        sc1 = scale_at(0, lane + 32, page_at(0, lane + 32));
-        pg0 = page_at(1, lane);
-        pg1 = page_at(1, lane + 32);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sc[i] = scale_at(0, i, page_at(0, i));
+          pg[i] = page_at(1, i);
+        }
       }
+      // e4m3: the exponent field of the largest scale so far, and the power of two that P is multiplied by for it
+      uint32_t top_exp = 7u;
+      float p_up = __uint_as_float((260u - 7u) << 23);
       float m_run = -INFINITY, l_part = 0.f;       // log2 domain; l_part: this thread's keys
       for (int j = 0; j < k.n; ++j) {
         const uint32_t at = jb + j;
         const int key0 = (k.blk0 + j) * BN + 64 * h;
         const uint32_t pages = __ballot_sync(0xffffffffu, entry >= 0 && entry < a.n_pages) >> (4 * h) & 0xFu;
         entry = entry_of(j + 1);
+        float o_down = 1.f;                        // e4m3: what O has to be multiplied by for a larger scale
         if constexpr (KV8) {
+          uint32_t top = __float_as_uint(fmaxf(max3(fabsf(sc[0]), fabsf(sc[1]), fabsf(sc[2])), fabsf(sc[3])));
+          top = min(__reduce_max_sync(0xffffffffu, top) >> 23, 250u);
+          if (top > top_exp) {                     // (the same in every thread of the CTA)
+            o_down = top - top_exp < 127u ? __uint_as_float((127u - (top - top_exp)) << 23) : 0.f;
+            top_exp = top;
+            p_up = __uint_as_float((260u - top) << 23);
+          }
           __syncwarp();
-          scale_s[lane] = sc0;
-          scale_s[lane + 32] = sc1;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            scale_s[lane + 32 * i] = sc[i];
+            scale_s[64 + lane + 32 * i] = sc[i] * p_up;
+          }
           __syncwarp();
-          sc0 = scale_at(j + 1, lane, pg0);
-          sc1 = scale_at(j + 1, lane + 32, pg1);
-          pg0 = page_at(j + 2, lane);
-          pg1 = page_at(j + 2, lane + 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sc[i] = scale_at(j + 1, i, pg[i]);
+            pg[i] = page_at(j + 2, i);
+          }
         }
         ok = __all_sync(0xffffffffu, wait(s_full, at & 1, a.status, abort_flag));
         if (!ok) break;
@@ -617,12 +703,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
         ok = exchange(mine, &other);
         if (!ok) break;
         const float mb = fmaxf(mine, other);
-        const bool move = mb > m_run + 8.f || (m_run == -INFINITY && mb != -INFINITY);
+        bool move = mb > m_run + 8.f || (m_run == -INFINITY && mb != -INFINITY);
         float corr = 1.f;
         if (move) {
           corr = m_run == -INFINITY ? 0.f : ex2(m_run - mb);
           l_part *= corr;
           m_run = mb;
+        }
+        if constexpr (KV8) {
+          corr *= o_down;
+          move = move || o_down != 1.f;
         }
         const float mu = m_run == -INFINITY ? 0.f : m_run;   // all masked so far: exp2(-inf) = 0
         // P of block at - 2 has been read: its product was issued before the scores of this block
@@ -640,11 +730,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
             p.y = ex2(p.y);
             ps[e & 1] = add2(ps[e & 1], p);
             if constexpr (KV8) {                   // V row = code * scale: the scale rides on P
-              const float2 k2 = reinterpret_cast<const float2*>(scale_s)[i >> 1];
+              const float2 k2 = reinterpret_cast<const float2*>(scale_s + 64)[i >> 1];
               p.x *= k2.x;
               p.y *= k2.y;
             }
-            w[e] = pack_bf16(p.x, p.y);
+            w[e] = KV8 ? pack_f16(p.x, p.y) : pack_bf16(p.x, p.y);
           }
           *reinterpret_cast<uint4*>(prow + ((u ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
@@ -683,7 +773,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
       tc_fence_after();
       const bool whole = k.n == k.all;
       const int slot = 2 * worker + (k.blk0 == 0);
-      const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      if constexpr (KV8) inv *= __uint_as_float((top_exp - 6u) << 23);   // 1 / p_up
       const int wrow = (warp & 1) * 32;            // the warp's first row
       // [32 rows][64 floats], 16-byte units XOR-swizzled by the row
       float4* tile_s = reinterpret_cast<float4*>(sP + warp * 8192);

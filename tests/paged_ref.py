@@ -62,7 +62,9 @@ class Cache:
         self.gen = g
         self.shape, self.dtype, self.wide = shape, dtype, wide
         self.k_scale = None
+        self.floor = None                                   # e4m3: see weight_floor
         if scales:
+            self.floor = []
             self.k_scale = torch.full((self.n_pages, P), float("nan"), device="cuda")
 
     def pool(self, spread=1.0):
@@ -84,10 +86,21 @@ class Cache:
                 view.view(torch.uint8)[page, slot] = codes.view(torch.uint8)
                 self.k_scale[page, slot] = sc
                 rows.append(codes.double() * sc.double()[:, None])
+                self.floor.append(weight_floor(codes, sc))
             else:
                 view[page, slot] = x.to(self.dtype)
                 rows.append(x.to(self.dtype).double())
         return view, rows
+
+
+def weight_floor(codes, scale):
+    """How far the smallest weights of an e4m3 cache move an output, by column: codes [n, d], scales [n].
+    A weight w = p s of a key with scale s (p <= 2^8, and p >= 1 for the largest, so the sum l is at least 1) is held
+    in fp16 as w 2^(6 - E), with 2^E <= max s: its values below 2^-14 are multiples of 2^-24, so it is off by at most
+    2^-25, that is w by 2^-25 2^(E - 6) <= 2^-31 max s. Each of the n keys adds that times its code, over l >= 1."""
+    if codes.shape[0] == 0:
+        return torch.zeros(codes.shape[1], dtype=torch.float64, device="cuda")
+    return 2.0 ** -31 * scale.double().max() * codes.double().abs().sum(0)
 
 
 def attend(q, lens, qlens, scale, k_rows, v_rows, dropped=()):
@@ -123,12 +136,15 @@ def attend(q, lens, qlens, scale, k_rows, v_rows, dropped=()):
     return o, lse, mag, big
 
 
-def check_attention(out, lse, want, d, n):
-    """The bound: P and the output are rounded to bf16 (half a step each); a score carries d fp32
-    roundings of its sum |q k|, which moves numerator and denominator; sums over n keys are fp32."""
+def check_attention(out, lse, want, d, n, floor=None):
+    """The bound: P and the output are rounded to bf16 (half a step each; P of an e4m3 cache to fp16, a finer one, with
+    an absolute error by column and sequence: floor); a score carries d fp32 roundings of its sum |q k|, which moves
+    numerator and denominator; sums over n keys are fp32."""
     o, l, mag, big = want
     delta = d * FP32 * big + 64 * FP32
     tol = BF16 * mag + BF16 * o.abs() + (2 * delta + (n + 16) * FP32) * mag
+    if floor:
+        tol = tol + torch.stack([f[:o.shape[-1]] for f in floor])[:, None, None]
     seen = ~torch.isnan(o)
     err = (out.double() - o).abs()
     worst = ((err - 1.01 * tol)[seen]).max().item() if seen.any() else 0.0

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from kv_indexing_b200 import lsa as L
-from tests.paged_ref import BF16, E4M3, FP32, Cache, attend, check_attention, ints, plan_numbers, rotate
+from tests.paged_ref import BF16, E4M3, FP32, Cache, attend, check_attention, ints, plan_numbers, rotate, weight_floor
 
 pytestmark = pytest.mark.gpu
 
@@ -34,7 +34,7 @@ def run(lens, qlens, Hq, Hkv, d, P, *, T=None, kind="bf16", seed=0, wide=0, scal
     assert L.lsa_device_status() == 0
     k = [r[:, None] for r in rows[0]] if latent else rows[0]
     v = [r[:, None, :512] for r in rows[0]] if latent else rows[1]
-    check_attention(out, lse, attend(q, lens, qlens, scale, k, v), d, max(lens))
+    check_attention(out, lse, attend(q, lens, qlens, scale, k, v), d, max(lens), c.floor)
     for b, n in enumerate(qlens):                          # rows behind a chunk stay as they were
         assert (out[b, n:] == 5.0).all() and (lse[b, n:] == 5.0).all()
     return c, q, pools, out, lse
@@ -83,6 +83,32 @@ def test_large_scores(d, kind, T):
     run([1000, 200], [T, T], 8, 1 if d == 576 else 4, d, 32, kind=kind, scale=2.0, spread=3.0)
 
 
+@pytest.mark.parametrize("T", [1, 40])
+@pytest.mark.parametrize("down", [1e-30, 1e-6, 1.0, 1e6, 1e30])
+def test_e4m3_queries_and_scales_of_any_size(T, down):
+    """Rows of q from 1e-30 to 1e30 and of zeros (fp16 holds neither end: they are scaled by row), keys whose scales
+    differ by 2^40, rising and falling along the sequence, and the product of the two kept moderate."""
+    lens, qlens = [900, 333], [T, T]
+    c = Cache(lens, 32, (576,), dtype=torch.float8_e4m3fn, scales=True, seed=T)
+    pool, _ = c.pool()
+    rows, c.floor = [], []
+    for b, n in enumerate(lens):
+        s = torch.arange(n, device="cuda")
+        page, slot = c.table[b].long()[s // 32], s % 32
+        sc = torch.exp2(torch.linspace(-30, 10, n, device="cuda") * (1 if b else -1) + (0 if b else -20)) * 0.01 / down
+        c.k_scale[page, slot] = sc
+        codes = pool.view(torch.uint8)[page, slot].view(pool.dtype)
+        rows.append(codes.double() * sc.double()[:, None])
+        c.floor.append(weight_floor(codes, sc))
+    q = (torch.randn(2, T, 8, 576, generator=c.gen, device="cuda") * down).to(torch.bfloat16)
+    q[:, :, 1] = 0.0
+    q[:, :, 2, 1:] = 0.0
+    out, lse = call(c, q, 0.02, [pool], qlens)
+    assert L.lsa_device_status() == 0
+    want = attend(q, lens, qlens, 0.02, [r[:, None] for r in rows], [r[:, None, :512] for r in rows])
+    check_attention(out, lse, want, 576, 900, c.floor)
+
+
 @pytest.mark.parametrize("d,kind", [(64, "bf16"), (128, "bf16"), (576, "bf16"), (576, "e4m3")])
 @pytest.mark.parametrize("T,n", [(1, 5000), (1, 300), (90, 700)])
 def test_rising_scores(d, kind, T, n):
@@ -114,7 +140,8 @@ def test_rising_scores(d, kind, T, n):
     assert L.lsa_device_status() == 0
     k = [r[:, None] for r in rows[0]] if d == 576 else rows[0]
     v = [r[:, None, :512] for r in rows[0]] if d == 576 else rows[1]
-    check_attention(out, lse, attend(q, [n], [T], 1.0, k, v), d, n)
+    floor = [weight_floor(x, torch.ones(n, device="cuda"))] if kind == "e4m3" else None
+    check_attention(out, lse, attend(q, [n], [T], 1.0, k, v), d, n, floor)
 
 
 @pytest.mark.parametrize("d,kind", [(64, "bf16"), (128, "bf16"), (576, "bf16"), (576, "e4m3")])
@@ -135,7 +162,7 @@ def test_unmapped_pages_are_left_out_and_reported(d, kind, T):
         L.lsa_device_status()
     k = [r[:, None] for r in rows[0]] if d == 576 else rows[0]
     v = [r[:, None, :512] for r in rows[0]] if d == 576 else rows[1]
-    check_attention(out, lse, attend(q, lens, qlens, d ** -0.5, k, v, dropped), d, 300)
+    check_attention(out, lse, attend(q, lens, qlens, d ** -0.5, k, v, dropped), d, 300, c.floor)
 
 
 @pytest.mark.parametrize("d", [64, 576])
@@ -178,7 +205,8 @@ def test_pools_past_32_bit_offsets(d, kind):
     assert L.lsa_device_status() == 0 and lse is None
     k = [r[:, None] for r in rows[0]] if d == 576 else rows[0]
     v = [r[:, None, :512] for r in rows[0]] if d == 576 else rows[1]
-    check_attention(out, None, attend(q, [n], [2], d ** -0.5, k, v), d, n)
+    floor = [weight_floor(x[:n], torch.ones(n, device="cuda"))] if kind == "e4m3" else None
+    check_attention(out, None, attend(q, [n], [2], d ** -0.5, k, v), d, n, floor)
 
 
 @pytest.mark.parametrize("d,kind", [(64, "bf16"), (128, "bf16"), (576, "bf16"), (576, "e4m3")])
