@@ -39,7 +39,7 @@
 //
 // e4m3: warps 4-5 load raw codes and warps 6-13 convert them for the products,
 // which take fp16 here: a code is an fp16 value, exactly, by one instruction per
-// pair (to bf16 it takes four, and they bound the kernel: 401 us where this takes
+// pair (to bf16 it takes four, and they bound the kernel: 401 us where this took
 // 379). q goes to fp16 times a power of two per row that brings its largest
 // column to [2^14, 2^15): exact but for columns 2^28 below that, by 2^-40 of it.
 // A key's scale multiplies its score and its P. P times the scale, with p at most
@@ -146,12 +146,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
 
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(&full[i], KV8 ? 8 : 2);
+      mbar_init(&full[i], KV8 ? 4 : 2);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&raw_full[i], 1);
-      mbar_init(&raw_empty[i], 4);
+      mbar_init(&raw_empty[i], 2);
     }
     mbar_init(s_full, 1);
     mbar_init(s_free, 8);
@@ -409,20 +409,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
         }
       } else {
         // --------------------------- e4m3: codes -> fp16, into the ring --
-        // Two groups of four warps take alternate slots, one code path for all of
-        // them (a path for K and one for V, with their codes in registers, ran at
-        // a sixth of an instruction a cycle). A lane converts 8 codes at a time;
-        // odd rows take a slot's chunks the other way round, so that two rows'
-        // reads do not meet in a bank.
-        const uint32_t group = (warp - 6) >> 2;
-        const int t = (tid - 192) & 127;
-        const int row = t >> 3, unit = t & 7;                    // rows row + 16 i
+        // Four groups of two warps take every fourth slot, one code path for all of
+        // them (two groups of four: 379 us where this takes 361; a path for K and one
+        // for V, with their codes in registers, ran at a sixth of an instruction a
+        // cycle). No more groups than slots: a group that is at slot `at` has filled
+        // at - 4, so at - 12 has been consumed and the parity of `empty` is not two
+        // phases old. A lane converts 8 codes at a time; odd rows take a slot's
+        // chunks the other way round, so that two rows' reads do not meet in a bank.
+        constexpr uint32_t kGroups = 4;
+        static_assert(kGroups <= kSlots && kRaw % kGroups == 0, "parities");
+        const uint32_t group = (warp - 6) >> 1;
+        const int t = (tid - 192) & 63;
+        const int row = t >> 3, unit = t & 7;                    // rows row + 8 i
         uint32_t seq = 0;                                        // slots before the piece
         for (Work k = *work_s; ok && k.n > 0; next_work<kRows, BN>(a, k)) {
           const Lens L = lens_of(a, k.bt / a.tiles);
           const uint32_t n = 9 * k.n;
 #pragma unroll 1
-          for (uint32_t i = (seq & 1) ^ group; i < n; i += 2) {
+          for (uint32_t i = (group - seq) % kGroups; i < n; i += kGroups) {
             // the ring takes K(0), then K(j + 1) (while there is one) and V(j) in turn
             int rows = 64, chunks = 2;                           // rows that count (V), chunks of the slot
             if (i == 4) {
@@ -444,8 +448,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
             const uint8_t* src = sRaw + rs * kChunk;
             uint8_t* dst = sRing + st * kSlot;
 #pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-              const int r = row + 16 * r4;
+            for (int r4 = 0; r4 < 8; ++r4) {
+              const int r = row + 8 * r4;
 #pragma unroll
               for (int cc = 0; cc < 2; ++cc) {
                 const int c = cc ^ (row & 1);
