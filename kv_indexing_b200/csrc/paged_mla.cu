@@ -17,10 +17,12 @@
 // contraction instead has the CTAs exchange 32 KB of partial scores per 64 keys;
 // that measured 5.2 us a block, ten times the products themselves.)
 //
-// Per block and CTA: 128 x 128 x (576 + 512) / 2 multiply-adds (2176 cycles at
-// 4096 a cycle) against shared memory at 128 bytes a cycle: operands of Q K^T
-// 12 x 4 and 24 x 2 KB, of P V 16 x 6 KB, staging 136 KB, P 16 KB: 344 KB, 2690
-// cycles. So shared memory bounds a full pipeline, at 0.8 of the tensor rate.
+// Per block and CTA: 128 x 128 x (576 + 512) / 2 multiply-adds, 2176 cycles at
+// 4096 a cycle; loads of 136 KB do not slow them. A block takes 3.1 K cycles, 2.3
+// K with the softmax left out: the issuing thread shares its scheduler with a
+// softmax warp. Back to back, the power cap bounds long calls (1.25 PFLOP/s for a
+// 500-token chunk over 32768 tokens; decode of 8 x 131072 tokens runs at 0.55 of
+// the tensor and 0.6 of the HBM rate at once, at 1.43 GHz).
 //
 // Tensor memory (512 columns): O 256, S 64, q's columns [0, 384) as the A operand
 // 192 (each row in lanes r and r + 64, as the pair's MMA reads it). Shared
