@@ -358,6 +358,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && u < n1) ok = product(1, u, n1, false);
           }
         }
+        // a half without steps waits here too: it must not load the next piece's q before the other has loaded this one's
+        if (ok && n0 == 0) umma_commit(&o_full[0]);
+        if (ok && n1 == 0) umma_commit(&o_full[1]);
         at0 += n0;
         at1 += n1;
       }
@@ -372,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + kColS + 128 * half + lane_base, tO = tmem + kColO + D * half + lane_base;
     const float c = a.scale_log2;
-    uint32_t seq0 = 0, done = 0, outs = 0;      // ring places, steps and pieces with steps of this half so far
+    uint32_t seq0 = 0, done = 0, outs = 0;      // ring places, steps and pieces of this half so far
     uint32_t mg = 0;                            // merge buffer uses so far
     // the warp's place in the list is kept in shared memory between pieces
     Work* my_work = work_s + 1 + warp;
@@ -549,11 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     seq0 += n_places;
     done += n_steps;
     if (!ok) break;
-    if (n_steps > 0) {
-      ok = __all_sync(0xffffffffu, wait(&o_full[half], outs & 1, a.status, abort_flag));
-      ++outs;
-      if (!ok) break;
-    }
+    ok = __all_sync(0xffffffffu, wait(&o_full[half], outs & 1, a.status, abort_flag));
+    ++outs;
+    if (!ok) break;
     tc_fence_after();
     const bool mine = r < rows;
     const Work k = *my_work;

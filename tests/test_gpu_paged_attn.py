@@ -29,6 +29,8 @@ def run(lens, qlens, Hq, Hkv, d, P, *, T=None, kind="bf16", seed=0, wide=0, scal
     pools, rows = zip(*[c.pool(spread) for _ in range(1 if latent else 2)])
     T = T or max(max(qlens), 1)
     q = torch.randn(len(lens), T, Hq, d, generator=c.gen, device="cuda").to(torch.bfloat16)
+    for b, n in enumerate(qlens):
+        q[b, n:] = float("nan")                            # behind a chunk: never used
     scale = scale or 1 / math.sqrt(d)
     out, lse = call(c, q, scale, pools, qlens)
     assert L.lsa_device_status() == 0
@@ -69,6 +71,14 @@ def test_chunks_of_many_rows(d, Hq, Hkv, kind, lens, qlens):
 @pytest.mark.parametrize("lens", [[30001], [9000, 20, 17000, 1]])
 def test_long_sequences_are_split(d, Hq, Hkv, kind, lens):
     run(lens, [1] * len(lens), Hq, Hkv, d, 64, kind=kind, seed=4)
+
+
+@pytest.mark.parametrize("d,Hq,Hkv,kind,T", [(64, 24, 24, "bf16", 1), (128, 4, 2, "bf16", 2), (128, 160, 1, "bf16", 2),
+                                             (576, 5, 1, "bf16", 1), (576, 5, 1, "e4m3", 2)])
+def test_many_sequences(d, Hq, Hkv, kind, T):
+    """More sequences than workers: a worker goes through many tiles, empty ones among them."""
+    lens = [(37 * i) % 290 for i in range(350)]
+    run(lens, [min(T, n) if i % 7 else 0 for i, n in enumerate(lens)], Hq, Hkv, d, 16, T=T, kind=kind, seed=9)
 
 
 @pytest.mark.parametrize("d,Hq,Hkv,kind", [(64, 4, 2, "bf16"), (128, 4, 2, "bf16"), (576, 16, 1, "bf16")])
