@@ -370,27 +370,22 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const int* ref, int
   const int words = (n_pages + 31) / 32;
   int* before = reinterpret_cast<int*>(live + words);
   __shared__ int live_below;                             // live pages below n_live
-  for (int w = threadIdx.x; w < words; w += kPlan) {
-    uint32_t m = 0u;
-    const int p0 = w * 32, np = min(32, n_pages - p0);
-    if (np == 32) {
-      int4 v[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // a warp takes 32 pages at a time, one per lane
+  for (int w0 = warp; w0 < words; w0 += 4 * (kPlan / 32)) {
+    int r[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = reinterpret_cast<const int4*>(ref + p0)[i];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        m |= (v[i].x > 0 ? 1u : 0u) << (4 * i) | (v[i].y > 0 ? 2u : 0u) << (4 * i) | (v[i].z > 0 ? 4u : 0u) << (4 * i) |
-             (v[i].w > 0 ? 8u : 0u) << (4 * i);
-        if (ref_out != ref) reinterpret_cast<int4*>(ref_out + p0)[i] = v[i];
-      }
-    } else {
-      for (int i = 0; i < np; ++i) {
-        const int r = ref[p0 + i];
-        m |= (r > 0 ? 1u : 0u) << i;
-        if (ref_out != ref) ref_out[p0 + i] = r;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int p = (w0 + i * (kPlan / 32)) * 32 + lane;
+      r[i] = p < n_pages ? ref[p] : 0;
     }
-    live[w] = m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int w = w0 + i * (kPlan / 32), p = w * 32 + lane;
+      const uint32_t m = __ballot_sync(0xffffffffu, r[i] > 0);
+      if (lane == 0 && w < words) live[w] = m;
+      if (p < n_pages && ref_out != ref) ref_out[p] = r[i];
+    }
   }
   __syncthreads();
   const int per = (words + kPlan - 1) / kPlan;           // consecutive words of a thread
@@ -415,23 +410,16 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const int* ref, int
   int* src = ws + kCompactHeader;
   int* dst = src + n_pages;
   int* map = dst + n_pages;
-  for (int p = n_live + threadIdx.x; p < n_pages; p += kPlan) map[p] = -1;
-  for (int w = threadIdx.x; w < words; w += kPlan) {
+  for (int w = warp; w < words; w += kPlan / 32) {
+    const int p = w * 32 + lane;
     const uint32_t m = live[w];
-    const int p0 = w * 32, np = min(32, n_pages - p0);
-    const uint32_t all = np == 32 ? 0xFFFFFFFFu : (1u << np) - 1u;
-    const uint32_t low = p0 + 32 <= n_live ? 0xFFFFFFFFu : (p0 >= n_live ? 0u : (1u << (n_live - p0)) - 1u);   // pages < n_live
-    uint32_t holes = ~m & low & all;
-    while (holes) {
-      const int i = __ffs(holes) - 1;
-      holes &= holes - 1;
-      dst[p0 + i - (before[w] + __popc(m & ((1u << i) - 1u)))] = p0 + i;
-    }
-    uint32_t movers = m & ~low;
-    while (movers) {
-      const int i = __ffs(movers) - 1;
-      movers &= movers - 1;
-      src[before[w] + __popc(m & ((1u << i) - 1u)) - live_below] = p0 + i;
+    const int rank = before[w] + __popc(m & ((1u << lane) - 1u));   // live pages below p
+    const bool alive = (m >> lane) & 1u;
+    if (p < n_live) {
+      if (!alive) dst[p - rank] = p;                     // a hole
+    } else if (p < n_pages) {
+      if (alive) src[rank - live_below] = p;             // a page to be moved
+      else map[p] = -1;
     }
   }
   __syncthreads();
