@@ -222,7 +222,8 @@ typedef struct lsa_append_in {
  * K row of token s: k + table[b, s / P] * k_page_stride + (s % P) * k_row_stride
  * + g * d_qk (elements), V alike. Supported: (d_qk, d_v) = (64, 64) and
  * (128, 128), bf16, Hq a multiple of Hkv; and latent rows (576, 512) with v = k, Hkv = 1,
- * Hq <= 128, bf16 or LSA_E4M3 (K = V = code * k_scale[page, slot], fp32).
+ * Hq <= 128, bf16 or LSA_E4M3 (K = V = code * k_scale[page, slot], fp32; scales may lie any number of
+ * octaves apart; columns of a query row below 2^-28 of its largest are rounded to 2^-39 of that).
  * q [B,T,Hq,d_qk] bf16, dense. Tokens of unmapped pages are left out. What a
  * page holds at and past seq_len is never used, whatever its bits; the rows of
  * cached tokens must be finite. A seq_len past the table's max_pages * P tokens

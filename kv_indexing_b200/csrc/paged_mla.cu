@@ -39,15 +39,19 @@
 // boxes at 7 TB/s over the GPU, two at 13, four at 19); the last warp of CTA 0
 // issues the MMAs.
 //
-// e4m3: warps 4-5 load raw codes and warps 6-13 convert them for the products,
-// which take fp16 here: a code is an fp16 value, exactly, by one instruction per
-// pair (to bf16 it takes four, and they bound the kernel: 401 us where this took
-// 379). q goes to fp16 times a power of two per row that brings its largest
-// column to [2^14, 2^15): exact but for columns 2^28 below that, by 2^-40 of it.
-// A key's scale multiplies its score and its P. P times the scale, with p at most
-// 2^8, is brought below 2^15 by a power of two that follows the largest scale so
-// far and rounded to fp16: to 2^-11, or by 2^-32 of the largest P where it is
-// below 2^-29 of it. All three powers of two are taken back in fp32.
+// e4m3: warps 4-5 load raw codes and warps 6-13 convert them for the products.
+// Scores take fp16: a code is an fp16 value, exactly, by one instruction per
+// pair. q goes to fp16 times a power of two per row that brings its largest
+// column to [2^14, 2^15): exact but for columns 2^28 below that, by 2^-39 of it.
+// V and P take bf16, three instructions per pair more (376 us for 4 x 2 queries
+// of 64 heads over 262144 ragged tokens, where V and P in fp16 took 361). A key's scale multiplies
+// its score and its P; scales of a cache may lie any number of octaves apart
+// (appending gives a row of zeros the scale 1, whatever the others have), and
+// the keys that make a row's output need not have the large ones. P times the
+// scale in fp16, even scaled by row, loses such weights: fp16 spans 2^30, bf16
+// has fp32's range. P is rounded to 2^-8 as for a bf16 cache. A power of two that
+// follows the largest scale so far keeps the accumulators in range and changes
+// no bit of P above 2^-126; it and q's are taken back in fp32.
 //
 // The running maximum moves only when a block raises it by more than 2^8 (P in
 // bf16 keeps its relative precision, sums are fp32), so O is rescaled rarely.
@@ -102,6 +106,11 @@ __device__ __forceinline__ uint32_t codes_to_f16(uint32_t four) {
   uint32_t h2;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(HIGH ? four >> 16 : four)));
   return h2;
+}
+// An fp16 pair that holds codes -> a bf16 pair, exact.
+__device__ __forceinline__ uint32_t f16_to_bf16(uint32_t h2) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+  return pack_bf16(f.x, f.y);
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -190,9 +199,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
     // issued: waiting for each in turn, with the products in between, took
     // longer (3700 cycles a block) than the products themselves.
     if (rank == 0 && elect_one()) {
-      constexpr uint32_t kType = KV8 ? 0 : 1;     // fp16, bf16
+      constexpr uint32_t kType = KV8 ? 0 : 1;     // of q and K: fp16, bf16
       const uint32_t idesc_qk = make_idesc(kType, kType, 128, BN, 0, 0);
-      const uint32_t idesc_pv = make_idesc(kType, kType, 128, 256, 0, 1);
+      const uint32_t idesc_pv = make_idesc(1, 1, 128, 256, 0, 1);
       const uint32_t hi = static_cast<uint32_t>(make_sdesc(0, 16, 1024, kLayoutSW128) >> 32);
       const uint32_t dQ = static_cast<uint32_t>(make_sdesc(smem_u32(sQ), 16, 1024, kLayoutSW128));
       const uint32_t dP = static_cast<uint32_t>(make_sdesc(smem_u32(sP), 16, 1024, kLayoutSW128));
@@ -410,11 +419,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
           }
         }
       } else {
-        // --------------------------- e4m3: codes -> fp16, into the ring --
-        // Four groups of two warps take every fourth slot, one code path for all of
-        // them (two groups of four: 379 us where this takes 361; a path for K and one
-        // for V, with their codes in registers, ran at a sixth of an instruction a
-        // cycle). No more groups than slots: a group that is at slot `at` has filled
+        // ------------------- e4m3: codes -> fp16 (K), bf16 (V), into the ring --
+        // Four groups of two warps take every fourth slot, any slot (two groups of four
+        // took 5 % longer; groups for K and groups for V, with their codes in registers,
+        // ran at a sixth of an instruction a cycle). No more groups than slots: a group that is at slot `at` has filled
         // at - 4, so at - 12 has been consumed and the parity of `empty` is not two
         // phases old. A lane converts 8 codes at a time; odd rows take a slot's
         // chunks the other way round, so that two rows' reads do not meet in a bank.
@@ -431,6 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
           for (uint32_t i = (group - seq) % kGroups; i < n; i += kGroups) {
             // the ring takes K(0), then K(j + 1) (while there is one) and V(j) in turn
             int rows = 64, chunks = 2;                           // rows that count (V), chunks of the slot
+            bool is_v = false;
             if (i == 4) {
               chunks = 1;
             } else if (i > 4) {
@@ -440,6 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
                 if (s == 4) chunks = 1;
               } else {
                 const int half = (last ? s : s - 5) >> 1;
+                is_v = true;
                 rows = L.len - (k.blk0 + j) * BN - half * 64;
               }
             }
@@ -449,19 +459,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
             if (!ok) break;
             const uint8_t* src = sRaw + rs * kChunk;
             uint8_t* dst = sRing + st * kSlot;
+            // (one test a slot: inside the loop K's codes would go through the longer way too)
+            auto convert = [&](auto to) {
 #pragma unroll
-            for (int r4 = 0; r4 < 8; ++r4) {
-              const int r = row + 8 * r4;
+              for (int r4 = 0; r4 < 8; ++r4) {
+                const int r = row + 8 * r4;
 #pragma unroll
-              for (int cc = 0; cc < 2; ++cc) {
-                const int c = cc ^ (row & 1);
-                if (c >= chunks) continue;
-                uint2 e = *reinterpret_cast<const uint2*>(src + r * 128 + c * 64 + unit * 8);
-                if (r >= rows) e = make_uint2(0u, 0u);           // past seq_len, whatever the page holds
-                *reinterpret_cast<uint4*>(dst + c * kChunk + r * 128 + ((unit ^ (r & 7)) << 4)) =
-                    make_uint4(codes_to_f16<0>(e.x), codes_to_f16<1>(e.x), codes_to_f16<0>(e.y), codes_to_f16<1>(e.y));
+                for (int cc = 0; cc < 2; ++cc) {
+                  const int c = cc ^ (row & 1);
+                  if (c >= chunks) continue;
+                  uint2 e = *reinterpret_cast<const uint2*>(src + r * 128 + c * 64 + unit * 8);
+                  if (r >= rows) e = make_uint2(0u, 0u);         // past seq_len, whatever the page holds
+                  *reinterpret_cast<uint4*>(dst + c * kChunk + r * 128 + ((unit ^ (r & 7)) << 4)) =
+                      make_uint4(to(codes_to_f16<0>(e.x)), to(codes_to_f16<1>(e.x)), to(codes_to_f16<0>(e.y)),
+                                 to(codes_to_f16<1>(e.y)));
+                }
               }
-            }
+            };
+            if (is_v) convert([](uint32_t h2) { return f16_to_bf16(h2); });
+            else convert([](uint32_t h2) { return h2; });
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -740,7 +756,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
               p.x *= k2.x;
               p.y *= k2.y;
             }
-            w[e] = KV8 ? pack_f16(p.x, p.y) : pack_bf16(p.x, p.y);
+            w[e] = pack_bf16(p.x, p.y);
           }
           *reinterpret_cast<uint4*>(prow + ((u ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
