@@ -125,10 +125,10 @@ typedef struct lsa_attn_in {
    * with the streaming prefix lsa_select_streaming writes for this sink and
    * window -- the sink tokens [0, min(sink, pos+1)) ascending, then the window
    * tokens up to pos ascending (LSA abstract (1), SI). The MLA kernel then
-   * computes those entries instead of reading them, and its work on them may
-   * overlap the kernel in the same stream that writes the rest of idx: that
-   * kernel may write idx only, and must not read or write this call's
-   * workspace or outputs (q, k, v and seq_len are read before it ends). A row
+   * computes those entries instead of reading them. Where the call before on the
+   * stream is a selection of this library (or a sparse attention) whose tensors
+   * and workspace are apart from this call's, its work on them overlaps that
+   * call's end; after any other call it starts when that has ended. A row
    * that breaks the promise gives undefined results. */
   int32_t stream_sink, stream_window;
   int32_t kv_dtype;        /* LSA_BF16 (0, the default) or LSA_E4M3 */

@@ -11,6 +11,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <unordered_map>
 
 #include "internal.h"
 #include "lsa.h"
@@ -341,6 +342,14 @@ lsa_status_t run_select(int mode, int B, int T, int L_max, const int* seq_len, c
   const SelectPlan p = mode == kSelectPages ? page_select_plan(B * T, n_slots, M)
                                             : token_select_plan(B * T, n_slots, bu);
   LSA_CHECK_CUDA(launch_select(a, p, sws, st, summary_ready && p.filter), "select launch");
+  Touched t;
+  const size_t rows = static_cast<size_t>(B) * T;
+  t.writes(out, rows * out_len * 4);
+  t.writes(sws, select_ws_bytes(static_cast<int>(rows), p));
+  t.reads(scores, rows * row_stride * 4);
+  t.reads(pages, pages ? rows * M * 4 : 0);
+  t.reads(seq_len, static_cast<size_t>(B) * 4);
+  leave_touched(st, t);
   return LSA_OK;
 }
 
@@ -477,8 +486,26 @@ lsa_status_t run_attn(const lsa_attn_in_t* ats, int n, const int* idx, int k, vo
       a.part_l = reinterpret_cast<float*>(w);
     }
   }
+  // What the splits that do not wait for idx touch, of every layer of the launch.
+  Touched t;
+  for (int i = 0; i < n; ++i) {
+    const lsa_attn_in_t* at = &ats[i];
+    const size_t heads = static_cast<size_t>(at->B) * at->T * at->Hq, kv_rows = static_cast<size_t>(at->B) * at->L_max;
+    const int es = at->kv_dtype == LSA_E4M3 ? 1 : 2;
+    t.writes(outs[i], heads * at->d_v * 2);
+    t.writes(lses ? lses[i] : nullptr, heads * 4);
+    t.writes(wss[i], attn_ws_bytes(at, k, n));
+    t.reads(at->q, heads * at->d_qk * 2);
+    t.reads(at->k, kv_rows * at->k_row_stride * es);
+    if (at->v != at->k) t.reads(at->v, kv_rows * at->v_row_stride * es);
+    t.reads(at->k_scale, kv_rows * 4);
+  }
+  t.reads(ats[0].seq_len, static_cast<size_t>(ats[0].B) * 4);
+  args[0].early = apart_from_last(st, t);
   LSA_CHECK_CUDA(launch_attn(maps, args, n, st), "attention launch");
   if (p.n_split > 1) LSA_CHECK_CUDA(launch_attn_combine(args, n, st), "attention combine launch");
+  t.reads(idx, static_cast<size_t>(ats[0].B) * ats[0].T * k * 4);
+  leave_touched(st, t);
   return LSA_OK;
 }
 
@@ -590,8 +617,47 @@ int device_sm_count() {
   return n;
 }
 
+namespace {
+struct LastLaunch {
+  int device;
+  Touched t;
+};
+std::mutex g_last_mutex;
+std::unordered_map<cudaStream_t, LastLaunch>& last_launches() {
+  static auto* m = new std::unordered_map<cudaStream_t, LastLaunch>;   // (outlives every static destructor)
+  return *m;
+}
+bool meet(const Touched::Range* a, int n_a, const Touched::Range* b, int n_b) {
+  for (int i = 0; i < n_a; ++i)
+    for (int j = 0; j < n_b; ++j)
+      if (a[i].lo < b[j].lo + b[j].bytes && b[j].lo < a[i].lo + a[i].bytes) return true;
+  return false;
+}
+}  // namespace
+
+void leave_touched(cudaStream_t stream, const Touched& t) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return;
+  std::lock_guard<std::mutex> lock(g_last_mutex);
+  last_launches()[stream] = LastLaunch{dev, t};
+}
+
+bool apart_from_last(cudaStream_t stream, const Touched& t) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  std::lock_guard<std::mutex> lock(g_last_mutex);
+  const auto it = last_launches().find(stream);
+  if (it == last_launches().end() || it->second.device != dev) return false;
+  const Touched& l = it->second.t;
+  return !meet(l.w, l.n_w, t.w, t.n_w) && !meet(l.w, l.n_w, t.r, t.n_r) && !meet(l.r, l.n_r, t.w, t.n_w);
+}
+
 cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void** args,
                        const cudaLaunchAttribute* extra, int n_extra) {
+  {
+    std::lock_guard<std::mutex> lock(g_last_mutex);
+    last_launches().erase(stream);
+  }
   cudaLaunchAttribute attr[3];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

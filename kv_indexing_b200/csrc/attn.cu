@@ -589,9 +589,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   cluster_sync_all();   // the partner's barriers are initialised before any remote arrive
-  // The index rows come from the previous kernel in the stream. The last cluster
-  // waits in any case, so this grid never completes before that kernel does.
-  if (!fixed || (blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)) pdl_wait();
+  // The index rows come from the previous kernel in the stream. Splits that need
+  // none of them go ahead where that kernel is known to leave the rest of their
+  // data alone (early). The last cluster waits in any case, so this grid never
+  // completes before that kernel does.
+  if (!fixed || !a.early || (blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1)) pdl_wait();
   pdl_trigger();
   // Second cluster phase: q is staged in the exchange buffers, so the partner
   // may copy scores into them only after this CTA has moved q into TMEM. The

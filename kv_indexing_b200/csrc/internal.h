@@ -167,6 +167,7 @@ struct AttnArgs {
   uint16_t* part_o;       // [rows, n_split, Hq, d_v] bf16, each split normalised by its own sum
   float* part_m;          // [rows, n_split, Hq]
   float* part_l;          // [rows, n_split, Hq]
+  int early;              // the kernel before this one on the stream leaves the prefix splits' data alone
   int* status;            // per-device status word
 };
 
@@ -304,5 +305,29 @@ cudaError_t set_max_smem(const void* func, size_t bytes);
 // finishes, and orders itself with pdl_wait before reading shared inputs.
 cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void** args,
                        const cudaLaunchAttribute* extra = nullptr, int n_extra = 0);
+
+// What the last kernel of a call reads and writes, for the one kernel that works before its predecessor has ended
+// (the sparse latent attention, on entries that it need not read from idx). It may do so only where that predecessor
+// is known and touches nothing that it touches: any other kernel of this library lets its dependents launch early
+// too, and may be writing q (lsa_rope), the cache (lsa_pages_append) or reading a workspace that the caller's
+// allocator has handed out again.
+struct Touched {
+  struct Range {
+    const uint8_t* lo;
+    size_t bytes;
+  };
+  static constexpr int kMax = 32;
+  Range w[kMax], r[kMax];
+  int n_w = 0, n_r = 0;
+  void writes(const void* p, size_t bytes) { add(w, &n_w, p, bytes); }
+  void reads(const void* p, size_t bytes) { add(r, &n_r, p, bytes); }
+  static void add(Range* list, int* n, const void* p, size_t bytes) {
+    if (p && bytes) list[(*n)++] = Range{static_cast<const uint8_t*>(p), bytes};
+  }
+};
+// The stream's last launch (every launch_pdl forgets what was known before it).
+void leave_touched(cudaStream_t stream, const Touched& t);
+// Whether the stream's last launch left a record, on this device, that `t` does not conflict with.
+bool apart_from_last(cudaStream_t stream, const Touched& t);
 
 }  // namespace lsa
