@@ -551,6 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   bool fixed = false;
   int f_sink_end = 0, f_wlo = 0;
   if (a.stream_sink + a.stream_window > 0 && nblk > 0) {
+    if (!a.early) pdl_wait();   // the lengths may come from the previous kernel too
     int L = __ldg(a.seq_len + b);
     L = L < 0 ? 0 : (L > a.L_max ? a.L_max : L);
     const int pos = L - a.T + (r - b * a.T);

@@ -108,3 +108,28 @@ def test_behind_in_a_graph():
             torch.cuda.synchronize()
         assert torch.equal(outs[0], ref[1]) and torch.equal(outs[1], ref[4])
     assert L.lsa_device_status() == 0
+
+
+def test_behind_a_fork_that_writes_the_lengths():
+    """4000 branches of one parent; the last four are the sequences of the attention, and only the fork gives them the
+    length that their index rows belong to."""
+    S, n = 4100, 4000
+    for seed in range(4):
+        s = Step(seed)
+        s.seq_len.fill_(LMAX)
+        s.idx = L.lsa_index_flat(s.iq, s.iw, s.ik, s.seq_len, BUDGET)
+        want = s.sparse()
+        table = torch.full((S, LMAX // P), -1, dtype=torch.int32, device="cuda")
+        table[0] = s.table[0]
+        ref = torch.zeros(B * LMAX // P, dtype=torch.int32, device="cuda")
+        ref[:LMAX // P] = 1
+        lens = torch.zeros(S, dtype=torch.int32, device="cuda")
+        lens[0] = LMAX
+        lens[-B:] = 1000
+        parent, child = torch.zeros(n, dtype=torch.int32, device="cuda"), torch.arange(S - n, S, device="cuda", dtype=torch.int32)
+        s.seq_len = lens[-B:]
+        torch.cuda.synchronize()
+        L.lsa_pages_fork(table, ref, lens, P, parent, child, [s.pool])
+        got = s.sparse()
+        assert torch.equal(got, want) and (lens[-n:] == LMAX).all()
+    assert L.lsa_device_status() == 0
