@@ -486,7 +486,8 @@ lsa_status_t lsa_pages_copy(const lsa_pool_t* pools, int32_t n_pools, int32_t n_
  * or above n_live moves to the k-th hole below it, in every pool, and table
  * entries and counts follow. table_out [S, max_pages] and ref_out [n_pages] may
  * be table and ref themselves; n_live (device int32) is optional. The pages
- * left behind keep their old contents. */
+ * left behind keep their old contents. A table entry that names a free page is
+ * unmapped and reported (another sequence's page may move there). */
 lsa_status_t lsa_pages_compact(const int32_t* table, const int32_t* ref, int32_t S, int32_t max_pages,
                                int32_t n_pages, const lsa_pool_t* pools, int32_t n_pools, int32_t* table_out,
                                int32_t* ref_out, int32_t* n_live, void* workspace, size_t workspace_bytes,

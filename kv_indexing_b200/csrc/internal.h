@@ -242,7 +242,7 @@ cudaError_t launch_copy(const Pools& pools, const int* src, const int* dst, cons
                         cudaStream_t stream);
 // ws: counters [2] (n_live, moves), then src [n_pages], dst [n_pages], map [n_pages]
 cudaError_t launch_compact_plan(const int* ref, int n_pages, int* ref_out, int* n_live, int* ws, cudaStream_t stream);
-cudaError_t launch_compact(const int* table, int S, int max_pages, int n_pages, int* table_out, const int* ws,
+cudaError_t launch_compact(const int* table, int S, int max_pages, int n_pages, int* table_out, int* ws,
                            const Pools& pools, int rows, int* status, cudaStream_t stream);
 constexpr int kCompactHeader = 64;   // ints before the lists
 

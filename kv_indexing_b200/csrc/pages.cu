@@ -359,6 +359,12 @@ __global__ void __launch_bounds__(kMove) copy_kernel(const int* __restrict__ src
 }
 
 // ------------------------------------------------------------------ compact --
+// The bits of the live pages, for the table entries: behind the pages to be moved, of which there are n_pages / 2 at
+// most (as many as holes below n_live).
+__device__ __forceinline__ uint32_t* live_words(int* ws, int n_pages) {
+  return reinterpret_cast<uint32_t*>(ws + kCompactHeader + n_pages - (n_pages + 31) / 32);
+}
+
 // One bit a page in shared memory (live or not) and the live pages before each
 // word. A hole below n_live and a live page at or above it of the same rank
 // make a move.
@@ -410,9 +416,11 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const int* ref, int
   int* src = ws + kCompactHeader;
   int* dst = src + n_pages;
   int* map = dst + n_pages;
+  uint32_t* live_out = live_words(ws, n_pages);
   for (int w = warp; w < words; w += kPlan / 32) {
     const int p = w * 32 + lane;
     const uint32_t m = live[w];
+    if (lane == 0) live_out[w] = m;
     const int rank = before[w] + __popc(m & ((1u << lane) - 1u));   // live pages below p
     const bool alive = (m >> lane) & 1u;
     if (p < n_live) {
@@ -434,7 +442,7 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(const int* ref, int
 
 // blocks [0, table_blocks): table entries; the rest: pieces of the moved pages
 __global__ void __launch_bounds__(kMove) compact_kernel(const int* table, long long entries, int n_pages,
-                                                        int* table_out, const int* __restrict__ ws,
+                                                        int* table_out, int* ws,
                                                         const __grid_constant__ Pools pools, int table_blocks,
                                                         int* status) {
   pdl_wait();
@@ -443,20 +451,18 @@ __global__ void __launch_bounds__(kMove) compact_kernel(const int* table, long l
   const int* src = ws + kCompactHeader;
   const int* dst = src + n_pages;
   const int* map = dst + n_pages;
+  const uint32_t* live = live_words(ws, n_pages);
   if (static_cast<int>(blockIdx.x) < table_blocks) {
     for (long long i = static_cast<long long>(blockIdx.x) * kMove + threadIdx.x; i < entries;
          i += static_cast<long long>(table_blocks) * kMove) {
       int e = table[i];
       if (e >= n_pages) {
         record_bad_page(status);
-      } else if (e >= n_live) {
-        // only a live page has a place to go; an entry of a free one is reported
-        const int d = map[e];
-        if (d >= 0) {
-          e = d;
-        } else {
-          record_bad_page(status);
-        }
+      } else if (e >= 0) {
+        // only a live page has a place; an entry of a free one would come to name another sequence's page
+        const int to = !((live[e >> 5] >> (e & 31)) & 1u) ? -1 : e >= n_live ? map[e] : e;
+        if (to < 0) record_bad_page(status);
+        e = to;
       }
       table_out[i] = e;
     }
@@ -527,7 +533,7 @@ cudaError_t launch_compact_plan(const int* ref, int n_pages, int* ref_out, int* 
                      static_cast<size_t>((n_pages + 31) / 32) * 8, stream, ref, n_pages, ref_out, n_live, ws);
 }
 
-cudaError_t launch_compact(const int* table, int S, int max_pages, int n_pages, int* table_out, const int* ws,
+cudaError_t launch_compact(const int* table, int S, int max_pages, int n_pages, int* table_out, int* ws,
                            const Pools& pools, int rows, int* status, cudaStream_t stream) {
   long long entries = rows ? static_cast<long long>(S) * max_pages : 0;
   const int sms = device_sm_count();

@@ -294,6 +294,19 @@ def test_compact(n_pages, live):
     assert torch.equal(table, t0) and torch.equal(ref, r0)
 
 
+def test_compact_unmaps_entries_of_free_pages():
+    """Stale entries on both sides of n_live: left alone they would name pages of other sequences afterwards."""
+    ref = torch.zeros(100, dtype=torch.int32, device="cuda")
+    ref[[0, 2, 40, 70, 99]] = 1                             # five live pages: holes at 1, 3 and 4
+    pool = torch.arange(100, device="cuda", dtype=torch.float32)[:, None].repeat(1, 8)
+    table = ints([[0, 40, 99], [2, 70, -1], [1, 4, 69]])    # the last row's pages are all free
+    t, r, n = L.lsa_pages_compact(table, ref, [pool])
+    with pytest.raises(L.LsaError, match="out of range"):
+        L.lsa_device_status()
+    assert n.tolist() == [5] and t.tolist() == [[0, 1, 4], [2, 3, -1], [-1, -1, -1]]
+    assert r.tolist() == [1] * 5 + [0] * 95 and pool[:5, 0].tolist() == [0, 40, 2, 70, 99]
+
+
 def test_wide_pages_past_32_bits():
     """A page of several pieces, and pools whose last pages lie past 4 GB."""
     pool = torch.zeros(70, 64 << 20, dtype=torch.uint8, device="cuda")
