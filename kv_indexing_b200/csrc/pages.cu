@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const PageArgs a, const 
         want = a.max_pages;
       }
       miss = want > 0 && a.table[static_cast<long long>(s) * a.max_pages + want - 1] < 0;
-      first[s] = want;
     }
+    int mapped_to = want;                                // entries [mapped_to, want) of this lane's row are unmapped
     unsigned todo = __ballot_sync(0xffffffffu, miss);
     while (todo) {
       const int l = __ffs(todo) - 1;
@@ -116,10 +116,12 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const PageArgs a, const 
         }
         end -= 32;
       }
-      if (lane == 0) first[ss] = end < 0 ? 0 : end;
+      if (lane == l) mapped_to = end < 0 ? 0 : end;
     }
-    __syncwarp();
-    if (s < a.S) upto[s] = want - first[s];
+    if (s < a.S) {
+      first[s] = mapped_to;
+      upto[s] = want - mapped_to;
+    }
   }
   __syncthreads();
   int need = 0;
