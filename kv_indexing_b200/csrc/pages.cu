@@ -124,14 +124,17 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const PageArgs a, const 
     }
   }
   __syncthreads();
+  // Counts stop at one more than there can be pages, which no rank reaches: 8192 rows of 2^19 entries have more than
+  // 32 bits hold.
+  const int most = a.n_pages + 1;
   int need = 0;
   for (int s0 = 0; s0 < a.S; s0 += kPlan) {
     const int s = s0 + threadIdx.x;
-    const int v = s < a.S ? upto[s] : 0;
+    const int v = s < a.S ? min(upto[s], most) : 0;
     int total;
     const int before = block_scan(v, &total);
-    if (s < a.S) upto[s] = need + before + v;
-    need += total;
+    if (s < a.S) upto[s] = min(need + before + v, most);
+    need = min(need + total, most);
   }
   __syncthreads();
   if (need == 0) return;

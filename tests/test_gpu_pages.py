@@ -236,6 +236,20 @@ def test_no_pages_left():
     d.check()
 
 
+def test_reserving_more_pages_than_32_bits_count():
+    """8192 rows that want 2^18 pages each: the first row takes what there is, and the rest is reported."""
+    S, M = 8192, 1 << 18
+    table = torch.full((S, M), -1, dtype=torch.int32, device="cuda")
+    ref = torch.zeros(64, dtype=torch.int32, device="cuda")
+    ref[5] = 1
+    L.lsa_pages_reserve(table, ref, torch.full((S,), 16 * M, dtype=torch.int32, device="cuda"), 16)
+    with pytest.raises(L.LsaError, match="ran out"):
+        L.lsa_device_status()
+    assert ref.tolist() == [1] * 64
+    assert table[0, :64].tolist() == list(range(5)) + list(range(6, 64)) + [-1]
+    assert int((table >= 0).sum()) == 63
+
+
 @pytest.mark.parametrize("n_pages,n", [(2, 1), (33, 5), (2000, 700), (2100, 1025), (1 << 19, 2000)])
 def test_copy(n_pages, n):
     g = torch.Generator(device="cuda").manual_seed(n)
