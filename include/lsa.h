@@ -464,7 +464,8 @@ lsa_status_t lsa_pages_reserve(int32_t* table, int32_t* ref, const int32_t* len,
  * reported if an id is out of range, an earlier pair has the same child, or the
  * parent is itself a child of this call. Without a free page left the child
  * keeps the full pages only, with seq_len cut to them (reported as by
- * lsa_pages_reserve). */
+ * lsa_pages_reserve). A parent's length past its row is reported and handed on
+ * clamped. */
 lsa_status_t lsa_pages_fork(int32_t* table, int32_t* ref, int32_t* seq_len, int32_t S, int32_t max_pages,
                             int32_t n_pages, int32_t page_size, const int32_t* parent, const int32_t* child,
                             int32_t n, const lsa_pool_t* pools, int32_t n_pools, void* workspace,

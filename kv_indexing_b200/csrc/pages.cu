@@ -206,6 +206,11 @@ __device__ __forceinline__ void move_piece(const Pools& pools, int c, int src, i
 }
 
 // --------------------------------------------------------------------- fork --
+// Tokens of a parent, at most what its row holds.
+__device__ __forceinline__ int fork_len(const PageArgs& a, int p) {
+  return min(max(0, a.seq_len[p]), a.max_pages * a.page_size);
+}
+
 // plan[i]: -2 = pair refused, -1 = no partly filled page, -3 = no free page for
 // it, else the page that takes the copy. shared memory: owner[S], the lowest
 // pair that names s as its child.
@@ -233,7 +238,8 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const PageArgs a, cons
         record_bad_page(a.status);
         code = -2;
       } else {
-        const int l = max(0, a.seq_len[p]);
+        const int l = fork_len(a, p);
+        if (l < a.seq_len[p]) record_bad_page(a.status);
         const int full = l / a.page_size;
         if (l - full * a.page_size > 0) {
           const int e = full < a.max_pages ? a.table[static_cast<long long>(p) * a.max_pages + full] : -1;
@@ -279,8 +285,8 @@ __global__ void __launch_bounds__(kMove) fork_kernel(const PageArgs a, const int
   const int code = plan[blockIdx.x];
   if (code == -2) return;
   const int p = parent[blockIdx.x], c = child[blockIdx.x];
-  const int l = max(0, a.seq_len[p]);
-  const int full = min(l / a.page_size, a.max_pages);
+  const int l = fork_len(a, p);
+  const int full = l / a.page_size;
   const int* from = a.table + static_cast<long long>(p) * a.max_pages;
   if (static_cast<int>(blockIdx.y) >= row_pieces) {
     if (code >= 0) move_piece(pools, blockIdx.y - row_pieces, from[full], code);

@@ -236,6 +236,23 @@ def test_no_pages_left():
     d.check()
 
 
+@pytest.mark.parametrize("past", [1, 15, 16, 4096])
+def test_fork_of_a_length_past_the_table(past):
+    """The child gets what the parent's row holds, and the length is reported, whole pages past it or not."""
+    m = Model(3, 4, 12, 16)
+    d = Device(m, 1)
+    m.reserve([64, 0, 0])
+    L.lsa_pages_reserve(d.table, d.ref, ints([64, 0, 0]), 16)
+    m.len = [64, 0, 0]
+    assert m.fork([0], [2])
+    d.len.copy_(ints([64 + past, 0, 0]))
+    L.lsa_pages_fork(d.table, d.ref, d.len, 16, ints([0]), ints([2]), d.pools)
+    with pytest.raises(L.LsaError, match="out of range"):
+        L.lsa_device_status()
+    m.len[0] += past
+    d.check()
+
+
 def test_reserving_more_pages_than_32_bits_count():
     """8192 rows that want 2^18 pages each: the first row takes what there is, and the rest is reported."""
     S, M = 8192, 1 << 18
