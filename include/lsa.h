@@ -444,7 +444,7 @@ lsa_status_t lsa_pages_append(const lsa_append_in_t* in, const lsa_rope_plan_t* 
 
 /* Attention over the paged cache (lsa_paged_attn_in_t). out [B,T,Hq,d_v] bf16;
  * lse [B,T,Hq] fp32 optional. A query that sees no token (pos < 0, or only
- * unmapped pages) gets out = 0, lse = -inf; rows t >= q_len[b] are left as they
+ * unmapped pages) gets out = 0, lse = -inf; one that holds a NaN and sees a token gets NaN; rows t >= q_len[b] are left as they
  * were. */
 lsa_status_t lsa_paged_attn(const lsa_paged_attn_in_t* in, void* out, float* lse, void* workspace,
                             size_t workspace_bytes, lsa_stream_t stream);

@@ -43,6 +43,9 @@
 // seq_len (whatever a page still holds there) are cleared in shared memory
 // before the product reads them: 0 * NaN is NaN. Unmapped pages are loaded from
 // past the pool's last page, which TMA fills with zeros, and masked.
+//
+// A row without keys has a sum of 0 and gets 0; a NaN of q makes the row's sum
+// NaN (its maximum, which ignores NaN, does not show it) and its output NaN.
 #include "paged.cuh"
 
 namespace lsa {
@@ -580,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (mine) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              reinterpret_cast<uint4*>(to)[i] = l_run > 0.f ? make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3])
+              reinterpret_cast<uint4*>(to)[i] = l_run != 0.f ? make_uint4(ov[4 * i], ov[4 * i + 1], ov[4 * i + 2], ov[4 * i + 3])
                                                             : make_uint4(0u, 0u, 0u, 0u);
           }
           mbar_arrive(mg_full);
@@ -610,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool whole = k.n == k.all;
     const int slot = 2 * worker + (k.blk0 == 0);
     const int prow = slot * kTile + (SHARED ? 128 * half : 0) + rt;
-    const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+    const float inv = l_run != 0.f ? 1.f / l_run : 0.f;
 #pragma unroll 1
     for (int c0 = 0; c0 < D; c0 += 32) {
       uint32_t ov[32];
@@ -622,12 +625,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
         if constexpr (!SHARED) ov[i] = w_own > 0.f ? __float_as_uint(__uint_as_float(ov[i]) * w_own) : 0u;
-        ov[i] = n_steps > 0 && l_run > 0.f ? __float_as_uint(__uint_as_float(ov[i]) * inv) : 0u;
+        ov[i] = n_steps > 0 && l_run != 0.f ? __float_as_uint(__uint_as_float(ov[i]) * inv) : 0u;
       }
       if constexpr (!SHARED) {
         ok = __all_sync(0xffffffffu, wait(mg_full, mg & 1, a.status, abort_flag));
         if (!ok) break;
-        if (mine && l_run > 0.f) {
+        if (mine && l_run != 0.f) {
           const float w = w_other * inv;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -661,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok) break;
     if (mine) {
       if (whole) {
-        if (a.lse) a.lse[orow] = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
+        if (a.lse) a.lse[orow] = l_run != 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
       } else {
         a.part_m[prow] = m_run;
         a.part_l[prow] = l_run;
@@ -730,7 +733,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedArgs a) {
     f[i] = 0.f;
     if (p < n_part) {
       f[i] = a.part_l[at(p)];
-      if (f[i] > 0.f) M = fmaxf(M, a.part_m[at(p)]);
+      if (f[i] != 0.f) M = fmaxf(M, a.part_m[at(p)]);
     }
   }
 #pragma unroll
@@ -739,12 +742,12 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedArgs a) {
 #pragma unroll
   for (int i = 0; i < kRegs; ++i) {
     const int p = i * 32 + lane;
-    if (f[i] > 0.f) f[i] *= exp2f(a.part_m[at(p)] - M);
+    if (f[i] != 0.f) f[i] *= exp2f(a.part_m[at(p)] - M);
     den += f[i];
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-  const float inv = den > 0.f ? 1.f / den : 0.f;
+  const float inv = den != 0.f ? 1.f / den : 0.f;
   const int col = (warp % kWarps) * 128 + lane * kPer;
   float acc[kPer];
 #pragma unroll
@@ -757,7 +760,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedArgs a) {
 #pragma unroll 8
     for (int p = 0; p < np; ++p) {
       const float w = __shfl_sync(0xffffffffu, f[i], p);
-      if (w > 0.f) {
+      if (w != 0.f) {
         const Vec o = *reinterpret_cast<const Vec*>(a.part_o + at(i * 32 + p) * DV + col);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) acc[e] = fmaf(o.v[e], w, acc[e]);
@@ -770,7 +773,7 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const PagedArgs a) {
   else
     *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
   if (a.lse && lane == 0 && warp % kWarps == 0)
-    a.lse[row] = den > 0.f ? (M + log2f(den)) * 0.69314718055994530942f : -INFINITY;
+    a.lse[row] = den != 0.f ? (M + log2f(den)) * 0.69314718055994530942f : -INFINITY;
 }
 
 }  // namespace

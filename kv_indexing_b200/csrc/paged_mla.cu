@@ -795,7 +795,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
       tc_fence_after();
       const bool whole = k.n == k.all;
       const int slot = 2 * worker + (k.blk0 == 0);
-      float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+      float inv = l_run != 0.f ? 1.f / l_run : 0.f;
       if constexpr (KV8) inv *= __uint_as_float((top_exp - 6u) << 23);   // 1 / p_up
       const int wrow = (warp & 1) * 32;            // the warp's first row
       // [32 rows][64 floats], 16-byte units XOR-swizzled by the row
@@ -811,7 +811,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
         for (int u = 0; u < 16; ++u) {
           const uint32_t* o = ov[u >> 3] + 4 * (u & 7);
           float4 w = make_float4(0.f, 0.f, 0.f, 0.f);      // a row without keys is 0
-          if (l_run > 0.f)
+          if (l_run != 0.f)
             w = make_float4(__uint_as_float(o[0]) * inv, __uint_as_float(o[1]) * inv, __uint_as_float(o[2]) * inv,
                             __uint_as_float(o[3]) * inv);
           tile_s[lane * 16 + (u ^ (lane & 15))] = w;
@@ -841,7 +841,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
       }
       if (h == 0 && row0 + r < rows) {
         if (whole) {
-          if (a.lse) a.lse[q0 + r] = l_run > 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
+          if (a.lse) a.lse[q0 + r] = l_run != 0.f ? (m_run + log2f(l_run)) * 0.69314718055994530942f : -INFINITY;
         } else {
           a.part_m[slot * kRows + rank * 64 + r] = m_run;
           a.part_l[slot * kRows + rank * 64 + r] = l_run;

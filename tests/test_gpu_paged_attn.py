@@ -254,6 +254,25 @@ def test_captured_call_follows_new_lengths(d, kind, T):
     assert L.lsa_device_status() == 0
 
 
+@pytest.mark.parametrize("d,Hq,Hkv,kind", [(64, 8, 2, "bf16"), (128, 6, 1, "bf16"), (576, 8, 1, "bf16"), (576, 8, 1, "e4m3")])
+@pytest.mark.parametrize("T", [1, 50])
+def test_queries_that_are_not_numbers(d, Hq, Hkv, kind, T):
+    """A NaN or an infinity in a query row makes that row NaN, in pieces that are merged too, and no other."""
+    lens, qlens = [5000, 200, 0], [T, T, T]
+    c, q, pools, out, lse = run(lens, qlens, Hq, Hkv, d, 32, kind=kind, seed=T)
+    bad = torch.zeros(3, T, Hq, dtype=torch.bool, device="cuda")
+    for i, (b, t, h, col, v) in enumerate([(0, T - 1, 1, 0, float("nan")), (0, 0, 2, d - 1, float("nan")),
+                                           (1, T // 2, 0, d // 2, float("nan")), (1, 0, 3, 5, float("inf")), (2, 0, 0, 1, float("nan"))]):
+        q[b, t, h, col] = v
+        bad[b, t, h] = b < 2
+    q[1, 0, 4] = float("nan")
+    bad[1, 0, 4] = True
+    o2, l2 = call(c, q, 1 / math.sqrt(d), pools, qlens)
+    assert L.lsa_device_status() == 0
+    assert torch.isnan(o2[bad]).all() and torch.isnan(l2[bad]).all()
+    assert torch.equal(o2[~bad], out[~bad]) and torch.equal(l2[~bad], lse[~bad])
+
+
 def test_stream_argument_orders_what_the_call_allocates():
     """Outputs and workspaces of a call on `stream` belong to that stream: the current one is busy for a while, and
     allocates right after the call."""
