@@ -11,7 +11,6 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
-#include <unordered_map>
 
 #include "internal.h"
 #include "lsa.h"
@@ -618,14 +617,21 @@ int device_sm_count() {
 }
 
 namespace {
+// One record a stream, streams that share a slot push one another out (a stream without a record only loses the early
+// start): no allocation, which could throw through the C entry, and nothing that grows with the streams of a program.
 struct LastLaunch {
+  cudaStream_t stream;
   int device;
+  bool known;
   Touched t;
 };
+constexpr int kLastSlots = 64;
+LastLaunch g_last[kLastSlots];
 std::mutex g_last_mutex;
-std::unordered_map<cudaStream_t, LastLaunch>& last_launches() {
-  static auto* m = new std::unordered_map<cudaStream_t, LastLaunch>;   // (outlives every static destructor)
-  return *m;
+LastLaunch& last_slot(cudaStream_t stream) {
+  uint64_t x = reinterpret_cast<uintptr_t>(stream);
+  x = (x ^ (x >> 4)) * 0x9E3779B97F4A7C15ull;   // (golden ratio: spreads the low bits upwards)
+  return g_last[x >> 58];
 }
 bool meet(const Touched::Range* a, int n_a, const Touched::Range* b, int n_b) {
   for (int i = 0; i < n_a; ++i)
@@ -639,16 +645,20 @@ void leave_touched(cudaStream_t stream, const Touched& t) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return;
   std::lock_guard<std::mutex> lock(g_last_mutex);
-  last_launches()[stream] = LastLaunch{dev, t};
+  LastLaunch& l = last_slot(stream);
+  l.stream = stream;
+  l.device = dev;
+  l.known = true;
+  l.t = t;
 }
 
 bool apart_from_last(cudaStream_t stream, const Touched& t) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   std::lock_guard<std::mutex> lock(g_last_mutex);
-  const auto it = last_launches().find(stream);
-  if (it == last_launches().end() || it->second.device != dev) return false;
-  const Touched& l = it->second.t;
+  const LastLaunch& last = last_slot(stream);
+  if (!last.known || last.stream != stream || last.device != dev) return false;
+  const Touched& l = last.t;
   return !meet(l.w, l.n_w, t.w, t.n_w) && !meet(l.w, l.n_w, t.r, t.n_r) && !meet(l.r, l.n_r, t.w, t.n_w);
 }
 
@@ -656,7 +666,8 @@ cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, size_t smem, cudaS
                        const cudaLaunchAttribute* extra, int n_extra) {
   {
     std::lock_guard<std::mutex> lock(g_last_mutex);
-    last_launches().erase(stream);
+    LastLaunch& l = last_slot(stream);
+    if (l.stream == stream) l.known = false;
   }
   cudaLaunchAttribute attr[3];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
