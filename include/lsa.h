@@ -182,7 +182,8 @@ typedef struct lsa_rope_plan {
 } lsa_rope_plan_t;
 
 /* Rows to rotate: x [B,T,H,d] and out alike, bf16 or fp32. Strides in elements
- * (the last dimension is dense); out may be x with x's strides. Columns
+ * (the last dimension is dense); out may be x with x's strides, else the two share
+ * no element, and no two rows of out do. Columns
  * [offset, offset + rot_dim) are rotated; the others are copied. */
 typedef struct lsa_rope_in {
   int32_t B, T, H, d;
