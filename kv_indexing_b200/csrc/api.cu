@@ -623,8 +623,10 @@ struct LastLaunch {
   cudaStream_t stream;
   int device;
   bool known;
+  uint64_t count;   // launches so far
   Touched t;
 };
+thread_local uint64_t t_count = 0;   // this thread's last launch among them
 constexpr int kLastSlots = 64;
 LastLaunch g_last[kLastSlots];
 std::mutex g_last_mutex;
@@ -646,6 +648,7 @@ void leave_touched(cudaStream_t stream, const Touched& t) {
   if (cudaGetDevice(&dev) != cudaSuccess) return;
   std::lock_guard<std::mutex> lock(g_last_mutex);
   LastLaunch& l = last_slot(stream);
+  if (l.count != t_count) return;   // another thread has launched since
   l.stream = stream;
   l.device = dev;
   l.known = true;
@@ -668,6 +671,7 @@ cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, size_t smem, cudaS
     std::lock_guard<std::mutex> lock(g_last_mutex);
     LastLaunch& l = last_slot(stream);
     if (l.stream == stream) l.known = false;
+    t_count = ++l.count;
   }
   cudaLaunchAttribute attr[3];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -325,7 +325,7 @@ struct Touched {
     if (p && bytes) list[(*n)++] = Range{static_cast<const uint8_t*>(p), bytes};
   }
 };
-// The stream's last launch (every launch_pdl forgets what was known before it).
+// The stream's last launch, this thread's last one too (every launch_pdl forgets what was known before it).
 void leave_touched(cudaStream_t stream, const Touched& t);
 // Whether the stream's last launch left a record, on this device, that `t` does not conflict with.
 bool apart_from_last(cudaStream_t stream, const Touched& t);

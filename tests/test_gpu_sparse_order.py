@@ -2,6 +2,8 @@
 
 Its prefix splits need no index row and may start before the selection in front of them has ended; behind any other
 call they have to wait. Every sequence of calls is compared with itself, the device waited for after each call."""
+import threading
+
 import pytest
 import torch
 
@@ -107,6 +109,37 @@ def test_behind_in_a_graph():
             ref.append(f(want))
             torch.cuda.synchronize()
         assert torch.equal(outs[0], ref[1]) and torch.equal(outs[1], ref[4])
+    assert L.lsa_device_status() == 0
+
+
+def test_two_threads_on_one_stream():
+    """One thread selects, the other rotates q and attends to it: neither knows what the other launches in between."""
+    got, want, other = Step(1), Step(1), Step(2)
+    rows = []
+    for _ in range(40):
+        rope(want)
+        rows.append(want.sparse())
+        torch.cuda.synchronize()
+    st, outs = torch.cuda.Stream(), []
+
+    def select():
+        with torch.cuda.stream(st):
+            for _ in range(120):
+                index(other)
+
+    def attend():
+        with torch.cuda.stream(st):
+            for _ in range(40):
+                rope(got)
+                outs.append(got.sparse())
+
+    threads = [threading.Thread(target=f) for f in (select, attend)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert len(outs) == 40 and all(torch.equal(a, b) for a, b in zip(outs, rows))
     assert L.lsa_device_status() == 0
 
 
