@@ -577,7 +577,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Lay<KV8>::kThreads, 
           ok = exchange(top, &other);
           if (!ok) break;
           const int e = 14 + 127 - static_cast<int>(__float_as_uint(fmaxf(top, other)) >> 23);
-          const int pow = max(-100, min(100, e));
+          // c stays a normal number: masked scores are -inf times c
+          const int pow = max(-100, min(min(100, e), static_cast<int>(__float_as_uint(a.scale_log2) >> 23) - 1));
           up = __uint_as_float(static_cast<uint32_t>(pow + 127) << 23);
           c = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - pow) << 23);
         }

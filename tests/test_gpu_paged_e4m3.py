@@ -104,3 +104,16 @@ def test_scales_2_to_the_120_apart(first, last):
     q = torch.randn(2, 3, 8, 576, generator=c.gen, device="cuda").to(torch.bfloat16)
     q[..., :512] = 0.0
     check(c, pool, q, [3, 3], 1.0)
+
+
+@pytest.mark.parametrize("scale", [1e-14, 1e-20, 1e-37])
+def test_rows_of_zeros_under_a_small_scale(scale):
+    """Equal weights: the scale times the power of two of a row of zeros (or of columns below 2^-86) stays above 0, which
+    a masked key's score of -inf is multiplied by."""
+    lens, qlens = [300, 40], [60, 40]
+    c = Cache(lens, 32, (576,), dtype=torch.float8_e4m3fn, scales=True)
+    pool, _ = c.pool()
+    q = torch.zeros(2, 60, 4, 576, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 1] = 2.0 ** -90
+    q[:, :, 2] = 1.0
+    check(c, pool, q, qlens, scale)
